@@ -93,6 +93,8 @@ typedef enum {
 #define OKV_DEV_BAD_POS 2u       /* position or length beyond the table    */
 #define OKV_DEV_BAD_SLOT 4u      /* sequence slot outside [0, num_seq_slots) */
 #define OKV_DEV_TIMEOUT 8u       /* a bulk copy did not land within ~1 s; the kernel gave up */
+#define OKV_DEV_NO_BLOCKS 16u    /* okv_plan_append: the free list ran out */
+#define OKV_DEV_NO_ROWS 32u      /* okv_plan_append: the token rows ran out */
 
 /* okv_append_quantize flags */
 #define OKV_PRE_ROTATED 1u  /* k, v are fp32 values already in the rotated basis */
@@ -333,6 +335,116 @@ okv_status okv_dequantize(const okv_cache_desc* desc, int32_t B, const int32_t* 
                           const int32_t* block_table, const int32_t* context_lens,
                           int32_t max_ctx, int32_t which, int32_t basis, int32_t source,
                           float* out, void* stream);
+
+/* Block tables and slot maps of a serving step, built on the GPU from request
+ * lengths: what okv_append_quantize, okv_decode_step and the attention calls
+ * take as seq_slot, pos, block_table, slot_lens and context_lens.  Request b
+ * of the step holds old = cached_lens[b] tokens in sequence slot seq_slot[b]
+ * and gains new = new_lens[b].  In the order of the requests:
+ *   - it takes ceil((old + new)/16) - ceil(old/16) blocks from the end of the
+ *     free list (free_blocks[count - 1] first, count = *free_count), written to
+ *     columns ceil(old/16) .. ceil((old + new)/16) - 1 of its block-table row;
+ *     other columns stay as they are;
+ *   - its tokens take the next `new` rows of tok_slot and tok_pos:
+ *     (slot, old), (slot, old + 1), ...; cu_tokens[b] is its first row;
+ *   - context_lens[b] = slot_lens[slot] = old + new.
+ * cu_tokens[num_requests] is the number of rows used, *free_count_out = count
+ * minus the blocks taken; rows behind the last token get slot = position = -1
+ * (padding rows: see OKV_PAD_ROWS).  The first request that the free list or
+ * the rows do not hold, and every later one, gets nothing and keeps its old
+ * length (OKV_DEV_NO_BLOCKS, OKV_DEV_NO_ROWS).  A request whose slot is -1 is
+ * padding: context_lens[b] = 0.  A request with another slot outside
+ * [0, num_seq_slots) or one that two requests name (OKV_DEV_BAD_SLOT, both are
+ * dropped), or with a negative or too long length (OKV_DEV_BAD_POS), is
+ * dropped the same way.  A count outside [0, num_free] is clamped into it; the
+ * ids in free_blocks are not looked at.
+ * The result does not depend on timing.  Only context_lens may be the same
+ * array as cached_lens, and free_count_out the same as free_count (a captured
+ * step that feeds itself); any other overlap is undefined.
+ *   workspace: device, okv_plan_workspace_bytes(num_requests) bytes (about 8
+ *   per request), 4-byte aligned; read only by the larger form of the call
+ *   (more than 2048 requests or 8192 rows), but a caller passes it always.
+ * One launch for small steps, two else.  Errors: INVALID_ARG (NULL, negative
+ * or too large sizes, misaligned arrays, workspace too small), UNSUPPORTED
+ * (num_seq_slots above OKV_PLAN_MAX_SLOTS).
+ * Pages: aiforradalom.hu, "OSCAR: figyelem-tudatos és bevetésre kész" (a paged
+ * cache with block tables under a serving engine). */
+#define OKV_PLAN_MAX_SLOTS 524288
+typedef struct {
+  int32_t num_requests;
+  int32_t max_tokens;          /* rows of tok_slot and tok_pos             */
+  int32_t num_seq_slots;       /* rows of block_table, entries of slot_lens */
+  int32_t max_blocks_per_seq;  /* row length of block_table                */
+  int32_t num_free;            /* entries of free_blocks                   */
+  const int32_t* seq_slot;     /* device [num_requests]                    */
+  const int32_t* cached_lens;  /* device [num_requests]                    */
+  const int32_t* new_lens;     /* device [num_requests]                    */
+  const int32_t* free_blocks;  /* device [num_free]                        */
+  const int32_t* free_count;   /* device [1]                               */
+  int32_t* block_table;        /* device [num_seq_slots][max_blocks_per_seq], updated */
+  int32_t* slot_lens;          /* device [num_seq_slots], updated          */
+  int32_t* context_lens;       /* device [num_requests], out               */
+  int32_t* cu_tokens;          /* device [num_requests + 1], out           */
+  int32_t* tok_slot;           /* device [max_tokens], out                 */
+  int32_t* tok_pos;            /* device [max_tokens], out                 */
+  int32_t* free_count_out;     /* device [1], out                          */
+  uint32_t* status_word;       /* device, nullable: OKV_DEV_* flags (OR-ed) */
+} okv_plan;
+size_t okv_plan_workspace_bytes(int32_t num_requests);
+okv_status okv_plan_append(const okv_plan* plan, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Norms of queries and keys for each head with the position rotation in the
+ * same pass: from a model's projections to what okv_append_quantize,
+ * okv_decode_step and okv_prefill_attention take as q, k and v.  For every
+ * token with position >= 0 and every head of 128 channels
+ *   y = x / sqrt(mean(x^2) + eps) * weight        (norm != 0; else y = x)
+ *   pairs (a, b) of y inside the first rot_dim channels become
+ *   (a cos - b sin, b cos + a sin) * rope_scale, angle = position * inv_freq[i];
+ * pair i is channels (i, i + rot_dim/2), or (2i, 2i + 1) with interleaved != 0.
+ * Values (v, nullable) are passed on without a norm or a rotation.
+ *   q, k, v: device, in_type, row (token, head) at token_stride * token +
+ *   head_stride * head elements (views of one fused projection need no copy),
+ *   each row 128 consecutive elements on a 16-byte boundary; q_out, k_out,
+ *   v_out: device bf16, contiguous [num_tokens][heads][128], 16-byte aligned;
+ *   each may be its own input where that is contiguous bf16, any other overlap
+ *   is undefined; positions: device int32 [num_tokens]; a row with a negative
+ *   position is padding, its outputs stay as they are; inv_freq: device fp32
+ *   [rot_dim/2]; q_weight, k_weight: device fp32 [128], NULL = 1.
+ * Angles are formed and reduced in fp64, sums and products are fp32, outputs
+ * are rounded once.  One launch.  Errors: INVALID_ARG (NULL, sizes, alignment,
+ * eps outside [0, 1], rope_scale not positive), UNSUPPORTED (head_dim != 128,
+ * rot_dim not a multiple of 16 up to 128, unknown in_type).
+ * Pages: gen-hub.ru "Что придумали в Together AI" (the rotations apply to the
+ * queries and keys that attention sees). */
+#define OKV_TYPE_BF16 0
+#define OKV_TYPE_FP16 1
+#define OKV_TYPE_FP32 2
+typedef struct {
+  int32_t num_tokens;
+  int32_t num_q_heads;
+  int32_t num_kv_heads;
+  int32_t head_dim;            /* must be 128                              */
+  int32_t in_type;             /* OKV_TYPE_* of q, k and v                 */
+  int32_t rot_dim;             /* rotated channels: a multiple of 16 in [0, 128] */
+  int32_t interleaved;         /* 0: pairs (i, i + rot_dim/2); 1: (2i, 2i + 1) */
+  int32_t norm;                /* 0: no norm                               */
+  float eps;
+  float rope_scale;            /* factor on cosines and sines (1 for plain RoPE) */
+  const void* q;
+  const void* k;
+  const void* v;               /* nullable, with v_out                     */
+  int64_t q_token_stride, q_head_stride; /* elements                       */
+  int64_t k_token_stride, k_head_stride;
+  int64_t v_token_stride, v_head_stride;
+  const int32_t* positions;
+  const float* inv_freq;
+  const float* q_weight;
+  const float* k_weight;
+  void* q_out;
+  void* k_out;
+  void* v_out;
+} okv_norm_rope;
+okv_status okv_qk_norm_rope(const okv_norm_rope* args, void* stream);
 
 /* Measurement hook: the next okv_decode_attention call made by this thread
  * records `start_event` just before its split-K attention kernel and

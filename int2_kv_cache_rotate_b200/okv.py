@@ -21,7 +21,7 @@ LIB_PATH = os.environ.get("OKV_LIBRARY") or os.path.join(_HERE, "libokv.so")
 HEADER = os.path.join(os.path.dirname(_HERE), "include", "okv.h")
 
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_CUDA, ERR_NUMERIC, ERR_IO = range(6)
-DEV_BAD_BLOCK, DEV_BAD_POS, DEV_BAD_SLOT, DEV_TIMEOUT = 1, 2, 4, 8
+DEV_BAD_BLOCK, DEV_BAD_POS, DEV_BAD_SLOT, DEV_TIMEOUT, DEV_NO_BLOCKS, DEV_NO_ROWS = 1, 2, 4, 8, 16, 32
 PRE_ROTATED = 1
 HEAD_DIM, BLOCK_TOKENS, WINDOW, BLOCK_HEAD_BYTES = 128, 16, 128, 1152
 
@@ -54,6 +54,25 @@ class CacheDesc(ctypes.Structure):
     ]
 
 
+class PlanArgs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("num_requests", "max_tokens", "num_seq_slots", "max_blocks_per_seq",
+                                              "num_free")] + \
+               [(n, ctypes.c_void_p) for n in ("seq_slot", "cached_lens", "new_lens", "free_blocks", "free_count",
+                                               "block_table", "slot_lens", "context_lens", "cu_tokens", "tok_slot",
+                                               "tok_pos", "free_count_out", "status_word")]
+
+
+class NormRopeArgs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("num_tokens", "num_q_heads", "num_kv_heads", "head_dim", "in_type",
+                                              "rot_dim", "interleaved", "norm")] + \
+               [("eps", ctypes.c_float), ("rope_scale", ctypes.c_float)] + \
+               [(n, ctypes.c_void_p) for n in ("q", "k", "v")] + \
+               [(n, ctypes.c_int64) for n in ("q_token_stride", "q_head_stride", "k_token_stride", "k_head_stride",
+                                              "v_token_stride", "v_head_stride")] + \
+               [(n, ctypes.c_void_p) for n in ("positions", "inv_freq", "q_weight", "k_weight", "q_out", "k_out",
+                                               "v_out")]
+
+
 _lib = None
 _P = ctypes.c_void_p
 _I32 = ctypes.c_int32
@@ -82,6 +101,9 @@ _SIGNATURES = {
     "okv_prefill_workspace_bytes": (_SZ, [_DESC, _I32]),
     "okv_prefill_attention": (_I32, [_DESC, _P, _I32, _I32, _I32, _P, _P, _P, _SZ, _P]),
     "okv_decode_step": (_I32, [_DESC, _P, _P, _I32, _P, _P, _P, _P, _I32, _P, _P, _P, _P, _P, _SZ, _P]),
+    "okv_plan_workspace_bytes": (_SZ, [_I32]),
+    "okv_plan_append": (_I32, [ctypes.POINTER(PlanArgs), _P, _SZ, _P]),
+    "okv_qk_norm_rope": (_I32, [ctypes.POINTER(NormRopeArgs), _P]),
     "okv_save_rotations": (_I32, [ctypes.c_char_p, _I32, _I32, _I32, _P, _P, ctypes.c_char_p]),
     "okv_rotations_file_shape": (_I32, [ctypes.c_char_p, _P, _P, _P, _P]),
     "okv_load_rotations": (_I32, [ctypes.c_char_p, _I32, _I32, _I32, _P, _P, _P, _SZ, _I32]),
@@ -125,6 +147,23 @@ def _stream(stream) -> int:
     if stream is None:
         stream = torch.cuda.current_stream()
     return stream.cuda_stream
+
+
+class _Same:
+    def __enter__(self):
+        pass
+
+    def __exit__(self, *exc):
+        pass
+
+
+_SAME = _Same()
+
+
+def _on(t):
+    """The device of tensor t as the current one (a launch and the current stream belong to the current device)."""
+    import torch
+    return _SAME if t.device.index == torch.cuda.current_device() else torch.cuda.device(t.device)
 
 
 def _need(t, dtype, name, device=True):
@@ -377,6 +416,125 @@ def prefill_attention(cache: Cache, q, slot: int, context_len: int, block_table,
     _check(lib().okv_prefill_attention(ctypes.byref(cache.desc), _ptr(q), T, int(slot), int(context_len),
                                        _ptr(block_table), _ptr(out), _ptr(ws), ws.numel(), _stream(stream)))
     return out
+
+
+class AppendPlan:
+    """Block tables and slot maps of serving steps of up to `batch` requests and
+    `max_tokens` new tokens, built on the GPU (okv_plan_append).  Holds the
+    outputs that the step's other calls take:
+
+      tok_slot, tok_pos  int32 [max_tokens]: sequence slot and position of every new token, -1 behind the last
+      context_lens       int32 [batch]: tokens of every request after the step
+      cu_tokens          int32 [batch + 1]: first token row of every request
+      free_count         int32 [1]: blocks left in the pool
+
+    The buffers stay the same from call to call, so a step can be captured in a
+    CUDA graph.  Two plans (or a plan built on two streams) share nothing."""
+
+    def __init__(self, batch: int, max_tokens: int, device="cuda"):
+        import torch
+        if batch < 0 or max_tokens < 0:
+            raise ValueError("batch and max_tokens must be >= 0")
+        self.batch, self.max_tokens = batch, max_tokens
+        i32 = dict(dtype=torch.int32, device=device)
+        self.tok_slot = torch.full((max_tokens,), -1, **i32)
+        self.tok_pos = torch.full((max_tokens,), -1, **i32)
+        self.context_lens = torch.zeros(batch, **i32)
+        self.cu_tokens = torch.zeros(batch + 1, **i32)
+        self.free_count = torch.zeros(1, **i32)
+        self.status = torch.zeros(4, **i32)
+        self.ws = torch.empty(int(lib().okv_plan_workspace_bytes(batch)), dtype=torch.uint8, device=device)
+        self._fn = lib().okv_plan_append
+        self._args = PlanArgs(num_requests=batch, max_tokens=max_tokens, context_lens=self.context_lens.data_ptr(),
+                              cu_tokens=self.cu_tokens.data_ptr(), tok_slot=self.tok_slot.data_ptr(),
+                              tok_pos=self.tok_pos.data_ptr(), free_count_out=self.free_count.data_ptr(),
+                              status_word=self.status.data_ptr())
+
+    def build(self, seq_slot, cached_lens, new_lens, block_table, slot_lens, free_blocks, free_count, stream=None):
+        """Plan one step: request b (sequence slot seq_slot[b], -1 for padding) holds cached_lens[b] tokens and
+        gains new_lens[b].  Updates block_table [slots][columns] and slot_lens [slots]; takes blocks from the end
+        of free_blocks[:free_count].  cached_lens may be this plan's context_lens and free_count its free_count
+        (a step that feeds the next).  Returns self."""
+        import torch
+        for name, t in (("seq_slot", seq_slot), ("cached_lens", cached_lens), ("new_lens", new_lens),
+                        ("block_table", block_table), ("slot_lens", slot_lens), ("free_blocks", free_blocks),
+                        ("free_count", free_count)):
+            _need(t, torch.int32, name)
+            if t.device != self.tok_slot.device:
+                raise ValueError(f"{name} must be on {self.tok_slot.device}")
+        for name, t in (("seq_slot", seq_slot), ("cached_lens", cached_lens), ("new_lens", new_lens)):
+            if t.shape != (self.batch,):
+                raise ValueError(f"{name} must have shape ({self.batch},), got {tuple(t.shape)}")
+        if block_table.dim() != 2 or slot_lens.shape != block_table.shape[:1]:
+            raise ValueError("block_table must be [slots][columns] and slot_lens [slots]")
+        if free_blocks.dim() != 1 or free_count.numel() != 1:
+            raise ValueError("free_blocks must be one-dimensional and free_count hold one value")
+        a = self._args
+        a.num_seq_slots, a.max_blocks_per_seq = block_table.shape
+        a.num_free = free_blocks.shape[0]
+        a.seq_slot, a.cached_lens, a.new_lens = seq_slot.data_ptr(), cached_lens.data_ptr(), new_lens.data_ptr()
+        a.block_table, a.slot_lens = block_table.data_ptr(), slot_lens.data_ptr()
+        a.free_blocks, a.free_count = free_blocks.data_ptr(), free_count.data_ptr()
+        with _on(self.tok_slot):
+            _check(self._fn(a, self.ws.data_ptr(), self.ws.numel(), _stream(stream)))
+        return self
+
+    def device_status(self) -> int:
+        return int(self.status[0].item())
+
+    def clear_status(self):
+        self.status.zero_()
+
+
+def qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps: float = 1e-6, v=None,
+                 interleaved: bool = False, norm: bool = True, rope_scale: float = 1.0, q_out=None, k_out=None,
+                 v_out=None, stream=None):
+    """Norms of queries and keys for each head with the position rotation (okv_qk_norm_rope): q [T][Hq][128], k and
+    v [T][Hkv][128] in bf16, fp16 or fp32, views of one fused projection included (the last dimension contiguous,
+    rows on 16-byte boundaries); positions int32 [T] (negative: a padding row, left as it is); inv_freq fp32
+    [rot_dim/2]; weights fp32 [128].  Returns contiguous bf16 (q, k), or (q, k, v) when v is given."""
+    import torch
+    kinds = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+    if q.dtype not in kinds:
+        raise TypeError(f"q must be bfloat16, float16 or float32, got {q.dtype}")
+    given = [("q", q), ("k", k)] + ([("v", v)] if v is not None else [])
+    for name, t in given:
+        if t.dtype != q.dtype:
+            raise TypeError(f"{name} must be {q.dtype} like q, got {t.dtype}")
+    for name, t in given:
+        if not t.is_cuda or t.device != q.device:
+            raise ValueError(f"{name} must be a CUDA tensor on one device with q")
+        if t.dim() != 3 or t.shape[0] != q.shape[0] or t.shape[2] != HEAD_DIM or (t.shape[2] and t.stride(2) != 1):
+            raise ValueError(f"{name} must be [T][heads][{HEAD_DIM}] with contiguous rows, got {tuple(t.shape)}")
+    if v is not None and v.shape[1] != k.shape[1]:
+        raise ValueError("k and v must have the same number of heads")
+    _need(positions, torch.int32, "positions"), _need(inv_freq, torch.float32, "inv_freq")
+    if positions.shape != q.shape[:1]:
+        raise ValueError(f"positions must have shape ({q.shape[0]},)")
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None:
+            _need(w, torch.float32, name)
+            if w.shape != (HEAD_DIM,):
+                raise ValueError(f"{name} must have shape ({HEAD_DIM},)")
+    for name, t in (("positions", positions), ("inv_freq", inv_freq), ("q_weight", q_weight), ("k_weight", k_weight)):
+        if t is not None and t.device != q.device:
+            raise ValueError(f"{name} must be on {q.device}")
+    outs = []
+    for (name, t), out in zip(given, (q_out, k_out, v_out)):
+        if out is None:
+            out = torch.empty(t.shape, dtype=torch.bfloat16, device=t.device)
+        _need(out, torch.bfloat16, name + "_out")
+        if out.shape != t.shape or out.device != q.device:
+            raise ValueError(f"{name}_out must have shape {tuple(t.shape)} on {q.device}")
+        outs.append(out)
+    st = [x for _, t in given for x in (t.stride(0), t.stride(1))] + ([0, 0] if v is None else [])
+    a = NormRopeArgs(q.shape[0], q.shape[1], k.shape[1], HEAD_DIM, kinds[q.dtype], 2 * inv_freq.numel(),
+                     int(interleaved), int(norm), eps, rope_scale, _ptr(q), _ptr(k), _ptr(v), *st, _ptr(positions),
+                     _ptr(inv_freq), _ptr(q_weight), _ptr(k_weight), _ptr(outs[0]), _ptr(outs[1]),
+                     _ptr(outs[2]) if v is not None else 0)
+    with _on(q):
+        _check(lib().okv_qk_norm_rope(a, _stream(stream)))
+    return tuple(outs)
 
 
 def time_next_decode_kernel(start_event, stop_event):
