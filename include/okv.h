@@ -59,6 +59,17 @@
  *   [1024 + 64 ng, 1024 + 128 ng) V scale and min, the same.
  * Block `blk`, head `h` starts at pages + (blk * num_kv_heads + h) *
  * okv_block_head_bytes(g).
+ * With OKV_INT4 the codes have 4 bits (s = fp16((max-min)/15), codes 0..15,
+ * two channels per byte: channel 2b in the low half of byte b, 2b + 1 in the
+ * high half; 4 + 32/g bits per element) and a block-head is 2048 + 128 ng
+ * bytes (2176, 2304 or 2560):
+ *   [   0, 1024) K codes, token-major: 16 rows of 64 bytes; 32-bit word w of a
+ *                row (bytes 4w .. 4w + 3) sits at word 4 (w & 3) + (w >> 2).
+ *   [1024, 2048) V codes: byte b of token t at 1024 + (b>>5)*512 +
+ *                ((b&7)*4 + (t>>2))*16 + ((b>>3)&3)*4 + (t&3).
+ *   [2048, 2048 + 128 ng) K, then V scale and min, as above.
+ * Every call takes either format; the window ring and the sink rows are the
+ * same for both.
  * Window ring: fp16 [num_seq_slots][num_kv_heads][2 (K,V)][W][d]; position p
  * of a sequence lives in row p % W; values are the rotated vector in fp16.
  * Sink rows: fp16 [num_seq_slots][num_kv_heads][2 (K,V)][num_sink][d];
@@ -99,6 +110,11 @@ typedef enum {
 /* okv_append_quantize flags */
 #define OKV_PRE_ROTATED 1u  /* k, v are fp32 values already in the rotated basis */
 
+/* format bits of okv_cache_desc.group, OR-ed with the group's channels */
+#define OKV_INT4 0x10000     /* 4-bit codes (else 2-bit)                     */
+#define OKV_OUT_BF16 0x20000 /* attention and dequantise outputs are bf16    */
+#define OKV_PAD_ROWS 0x40000 /* appended rows whose slot is -1 are padding   */
+
 #define OKV_HEAD_DIM 128
 #define OKV_BLOCK_TOKENS 16
 #define OKV_WINDOW 128
@@ -109,7 +125,8 @@ typedef struct {
   int32_t num_q_heads;        /* Hq; a multiple of num_kv_heads            */
   int32_t num_kv_heads;       /* Hkv                                        */
   int32_t head_dim;           /* must be 128                                */
-  int32_t group;              /* quantisation group: 128, 64 or 32 channels */
+  int32_t group;              /* quantisation group: 128, 64 or 32 channels,
+                                 OR-ed with format bits (OKV_INT4, ...)    */
   int32_t block_tokens;       /* must be 16                                 */
   int32_t window;             /* must be 128                                */
   int32_t num_blocks;         /* physical blocks in `pages`                 */
@@ -117,7 +134,7 @@ typedef struct {
   int32_t max_blocks_per_seq; /* row length of every block table            */
   int32_t num_sink;           /* sink tokens kept fp16: a multiple of 16 in
                                  [0, OKV_MAX_SINK], else OKV_ERR_UNSUPPORTED */
-  void* pages;                /* device, num_blocks*Hkv*1152 B, 16-B aligned */
+  void* pages;                /* device, okv_pages_bytes B, 16-B aligned    */
   void* window_ring;          /* device fp16, layout above, 16-B aligned     */
   const float* u_k;           /* device fp32 [Hkv][d][d]: U_K of each KV head */
   const float* u_v;           /* device fp32 [Hkv][d][d]: U_V of each KV head */
@@ -178,7 +195,8 @@ okv_status okv_load_rotations(const char* path, int32_t num_layers, int32_t num_
                               float* u_v, char* tag, size_t tag_capacity, int32_t verify);
 
 /* Bytes of one block-head (16 tokens of one KV head) for quantisation group
- * `group` (1152, 1280, 1536 for 128, 64, 32), 0 for an unsupported group.
+ * `group` (1152, 1280, 1536 for 128, 64, 32; 2176, 2304, 2560 with OKV_INT4;
+ * other format bits do not matter), 0 for an unsupported group.
  * The pages' INT2 format with a scale and a minimum per group (bigsaas.top,
  * "Revolução no Serviço de LLMs…", section "Resultados e Métricas de
  * Desempenho"). */
@@ -249,7 +267,7 @@ size_t okv_decode_workspace_bytes(const okv_cache_desc* desc, int32_t B);
  * gen-hub.ru "Что придумали в Together AI" (rotations of Q and of SV). */
 okv_status okv_decode_attention(const okv_cache_desc* desc, const void* q, int32_t B,
                                 const int32_t* seq_slot, const int32_t* block_table,
-                                const int32_t* context_lens, float* out, void* workspace,
+                                const int32_t* context_lens, void* out, void* workspace,
                                 size_t workspace_bytes, void* stream);
 
 /* Size of the device array behind okv_decode_attention_noalloc (8 MiB).  A
@@ -272,7 +290,7 @@ okv_status okv_decode_attention(const okv_cache_desc* desc, const void* q, int32
 okv_status okv_decode_step(const okv_cache_desc* desc, const void* k, const void* v, int32_t T,
                            const int32_t* new_seq_slot, const int32_t* new_pos, const int32_t* slot_lens,
                            const void* q, int32_t B, const int32_t* seq_slot, const int32_t* block_table,
-                           const int32_t* context_lens, float* out, void* workspace, size_t workspace_bytes,
+                           const int32_t* context_lens, void* out, void* workspace, size_t workspace_bytes,
                            void* stream);
 
 /* Decode attention that allocates nothing and takes no workspace.  The pages
@@ -293,7 +311,7 @@ okv_status okv_decode_step(const okv_cache_desc* desc, const void* k, const void
  *   serialised by the caller. */
 okv_status okv_decode_attention_noalloc(const okv_cache_desc* desc, const void* q, int32_t B,
                                         const int32_t* seq_slot, const int32_t* block_table,
-                                        const int32_t* context_lens, float* out, void* stream);
+                                        const int32_t* context_lens, void* out, void* stream);
 
 /* Chunked-prefill attention over the cache, for one sequence.  The chunk's
  * T tokens must already be appended (okv_append_quantize), so sequence
@@ -303,7 +321,7 @@ okv_status okv_decode_attention_noalloc(const okv_cache_desc* desc, const void* 
  * holds it at length L: positions [0, min(S, L)) from the sink rows,
  * [max(L - W, S), L) from the window ring, the rest from INT2 blocks.  As in
  * decode, q~ = q R_K and o = softmax(q~ x^T / sqrt(d)) x_V R_V^T.
- *   q: device bf16 [T][Hq][d]; slot, context_len: host ints (T <= L <=
+ *   q: device bf16 [T][Hq][d], 16-byte aligned; slot, context_len: host ints (T <= L <=
  *   max_blocks_per_seq * 16); block_table: device, as above; out: device
  *   fp32 [T][Hq][d]; workspace: device, at least
  *   okv_prefill_workspace_bytes(desc, T) bytes, 256-B aligned.
@@ -318,7 +336,7 @@ okv_status okv_decode_attention_noalloc(const okv_cache_desc* desc, const void* 
  * gen-hub.ru "Что придумали в Together AI" (the rotations of Q and of SV). */
 size_t okv_prefill_workspace_bytes(const okv_cache_desc* desc, int32_t T);
 okv_status okv_prefill_attention(const okv_cache_desc* desc, const void* q, int32_t T, int32_t slot,
-                                 int32_t context_len, const int32_t* block_table, float* out, void* workspace,
+                                 int32_t context_len, const int32_t* block_table, void* out, void* workspace,
                                  size_t workspace_bytes, void* stream);
 
 /* Gather and dequantise the cache into dense fp32 (the INT2 format's inverse:
@@ -334,7 +352,7 @@ okv_status okv_prefill_attention(const okv_cache_desc* desc, const void* q, int3
 okv_status okv_dequantize(const okv_cache_desc* desc, int32_t B, const int32_t* seq_slot,
                           const int32_t* block_table, const int32_t* context_lens,
                           int32_t max_ctx, int32_t which, int32_t basis, int32_t source,
-                          float* out, void* stream);
+                          void* out, void* stream);
 
 /* Block tables and slot maps of a serving step, built on the GPU from request
  * lengths: what okv_append_quantize, okv_decode_step and the attention calls

@@ -11,6 +11,8 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -30,18 +32,26 @@ def nvcc() -> str:
 
 
 def build(verbose_ptxas: bool = False, out: str = LIB, short_wait: bool = False) -> str:
-    srcs = [os.path.join(CSRC, s) for s in SOURCES]
     defs = ["-DOKV_WAIT_LIMIT_LOG2=6"] if short_wait else []
-    cmd = [nvcc(), *ARCH, "-O3", "-lineinfo", "-std=c++17", "-shared", *defs,
-           "-Xcompiler", "-fPIC,-fopenmp,-O3", "-I", os.path.join(ROOT, "include"), "-I", CSRC,
-           "-o", out, *srcs, "-lgomp"]
+    flags = [nvcc(), *ARCH, "-O3", "-lineinfo", "-std=c++17", *defs, "-Xcompiler", "-fPIC,-fopenmp,-O3",
+             "-I", os.path.join(ROOT, "include"), "-I", CSRC]
     if verbose_ptxas:
-        cmd.insert(1, "-Xptxas=-v")
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    if res.returncode != 0:
-        raise RuntimeError("nvcc failed:\n" + " ".join(cmd) + "\n" + res.stdout + res.stderr)
+        flags.insert(1, "-Xptxas=-v")
+
+    def run(cmd):
+        res = subprocess.run(cmd, capture_output=True, text=True)
+        if res.returncode != 0:
+            raise RuntimeError("nvcc failed:\n" + " ".join(cmd) + "\n" + res.stdout + res.stderr)
+        return res.stderr
+
+    with tempfile.TemporaryDirectory() as tmp:  # one object per source, compiled side by side, then linked
+        objs = [os.path.join(tmp, s + ".o") for s in SOURCES]
+        with ThreadPoolExecutor(len(SOURCES)) as pool:
+            logs = list(pool.map(lambda so: run([*flags, "-c", os.path.join(CSRC, so[0]), "-o", so[1]]),
+                                 zip(SOURCES, objs)))
+        run([nvcc(), *ARCH, "-shared", "-o", out, *objs, "-lgomp"])
     if verbose_ptxas:
-        sys.stderr.write(res.stderr)
+        sys.stderr.write("".join(logs))
     return out
 
 

@@ -1,5 +1,5 @@
 // Append kernels: rotate (U, Hadamard butterfly, bit-reversal remap), quantise
-// to INT2 with fp16 scale/min, pack, and write the paged cache and fp16 window.
+// to INT2 or INT4 with fp16 scale/min, pack, and write the paged cache and fp16 window.
 // Decode steps (a few tokens) run the CUDA-core kernel; prefill chunks of 128
 // tokens or more run the tensor-core kernel, which takes R either from the
 // cache's staged image (okv_build_r_image) or stages it from U per CTA.
@@ -75,6 +75,7 @@ __device__ __forceinline__ int tc_column(int b, int f) {
 // min/max reduction runs over that many lanes of the quad.  It runs on every
 // lane (the quad shuffles need all of them); `live` then gates validation
 // and the stores.
+template <int BITS>
 __device__ __forceinline__ void finish_token_tc(const AppendArgs& a, int tok, bool live, int h, int kind,
                                                 const float (&v)[8][4], int t) {
   float mn = v[0][0], mx = v[0][0];
@@ -97,7 +98,7 @@ __device__ __forceinline__ void finish_token_tc(const AppendArgs& a, int tok, bo
   const int slot = a.seq_slot[tok];
   const int p = a.pos[tok];
   if (slot < 0 || slot >= a.num_slots) {
-    if (t == 0) raise_flag(a.status, OKV_DEV_BAD_SLOT);
+    if (t == 0 && !(a.pad && slot == -1)) raise_flag(a.status, OKV_DEV_BAD_SLOT);
     return;
   }
   const int len = a.slot_lens[slot];
@@ -111,13 +112,24 @@ __device__ __forceinline__ void finish_token_tc(const AppendArgs& a, int tok, bo
     return;
   }
   // the quantiser's steps, in the same fp32 operations as quantize_warp
-  const float s32 = __fdiv_rn(__fsub_rn(mx, mn), 3.0f);
+  const float s32 = __fdiv_rn(__fsub_rn(mx, mn), BITS == 4 ? 15.0f : 3.0f);
   const __half s16 = fp16_sat(s32);
   const __half m16 = fp16_sat(mn);
   const float s = __half2float(s16);
   const float m = __half2float(m16);
-  uint32_t w[2] = {0u, 0u};
-  if (s != 0.0f) {
+  uint32_t w[BITS] = {};  // the lane's 8 or 16 code bytes
+  if constexpr (BITS == 4) {
+    if (s != 0.0f) {
+      const float r = __fdiv_rn(1.f, s);
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+#pragma unroll
+        for (int f = 0; f < 4; ++f)
+          w[k >> 1] += int4_code_magic(__fsub_rn(v[k][f], m), r, s) << (16 * (k & 1) + 4 * f);
+#pragma unroll
+      for (int k = 0; k < BITS; ++k) w[k] -= code_magic_sum(8);
+    }
+  } else if (s != 0.0f) {
     const CodeThresholds th = code_thresholds(s);
 #pragma unroll
     for (int k = 0; k < 8; ++k)
@@ -126,14 +138,23 @@ __device__ __forceinline__ void finish_token_tc(const AppendArgs& a, int tok, bo
   }
   uint8_t* base = a.pages + ((size_t)blk * a.hkv + h) * a.bhb;
   const int sl = p & 15;
-  if (kind == 0) {
+  if constexpr (BITS == 4) {
+    // bytes 16 t .. 16 t + 15: words 4 t + j of the row
+    if (kind == 0) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) *reinterpret_cast<uint32_t*>(base + sl * 64 + 16 * j + 4 * t) = w[j];
+    } else {
+#pragma unroll
+      for (int k = 0; k < 16; ++k) base[v4_code_offset(sl, 16 * t + k)] = (uint8_t)(w[k >> 2] >> (8 * (k & 3)));
+    }
+  } else if (kind == 0) {
     *reinterpret_cast<uint2*>(base + kKcOff + sl * 32 + 8 * t) = make_uint2(w[0], w[1]);
   } else {
 #pragma unroll
     for (int k = 0; k < 8; ++k) base[v_code_offset(sl, 8 * t + k)] = (uint8_t)(w[k >> 2] >> (8 * (k & 3)));
   }
   if ((t & (4 / a.ng - 1)) == 0)  // the first lane of each group
-    *reinterpret_cast<uint32_t*>(base + sm_offset(a.ng, kind, sl, t * a.ng / 4)) =
+    *reinterpret_cast<uint32_t*>(base + sm_offset(a.ng, kind, sl, t * a.ng / 4, BITS)) =
         (uint32_t)__half_as_ushort(s16) | ((uint32_t)__half_as_ushort(m16) << 16);
   __half* wrow = window_row(a, slot, h, kind, p, len);
   __half* srow = sink_row(a, slot, h, kind, p);
@@ -162,6 +183,7 @@ __device__ __forceinline__ void finish_token_tc(const AppendArgs& a, int tok, bo
 
 // Grid (ceil(T / tokens_per_cta), Hkv, 2); a CTA stages R once and runs
 // rounds of 128 tokens (16 per warp) over its token range.
+template <int BITS>
 __global__ void __launch_bounds__(kTcWarps * 32, 2) append_tc_kernel(AppendArgs a, int T, int tokens_per_cta) {
   extern __shared__ __align__(16) unsigned char tc_smem[];
   __nv_bfloat16* rs = reinterpret_cast<__nv_bfloat16*>(tc_smem);  // [3][128 c][136]: R split in three
@@ -245,7 +267,7 @@ __global__ void __launch_bounds__(kTcWarps * 32, 2) append_tc_kernel(AppendArgs 
       for (int k = 0; k < 8; ++k)
 #pragma unroll
         for (int f = 0; f < 4; ++f) v[k][f] = d[2 * k + (f >> 1)][2 * half + (f & 1)];
-      finish_token_tc(a, half ? tb : ta, half ? vb : va, h, kind, v, t);
+      finish_token_tc<BITS>(a, half ? tb : ta, half ? vb : va, h, kind, v, t);
     }
   }
 }
@@ -354,7 +376,7 @@ __device__ __forceinline__ void um_tma_load_3d(uint32_t dst, const CUtensorMap* 
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
       : "memory");
 }
-template <int NG>
+template <int NG, int BITS>
 __global__ void __launch_bounds__(kUmThreads, 1) append_umma_kernel(AppendArgs a, int T,
                                                                      const __grid_constant__ CUtensorMap map_k,
                                                                      const __grid_constant__ CUtensorMap map_v) {
@@ -527,7 +549,7 @@ __global__ void __launch_bounds__(kUmThreads, 1) append_umma_kernel(AppendArgs a
       // `valid` gates the stores (a token past T, or a bad destination)
       bool valid = tok < T;
       if (valid && !slot_ok) {
-        raise_flag(a.status, OKV_DEV_BAD_SLOT);
+        if (!(a.pad && slot == -1)) raise_flag(a.status, OKV_DEV_BAD_SLOT);
         valid = false;
       } else if (valid && !pos_ok) {
         raise_flag(a.status, OKV_DEV_BAD_POS);
@@ -539,7 +561,7 @@ __global__ void __launch_bounds__(kUmThreads, 1) append_umma_kernel(AppendArgs a
       // per group (NG per vector, 128 / NG channels each): min and max, the
       // fp16 scale and minimum, and the codes
       constexpr int GW = kD / NG;
-      uint32_t w[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};  // the 32 code bytes of the token
+      uint32_t w[4 * BITS] = {};                          // the 32 or 64 code bytes of the token
       uint32_t smg[NG];                                    // (scale, min) bits of each group
 #pragma unroll
       for (int k = 0; k < NG; ++k) {
@@ -560,13 +582,22 @@ __global__ void __launch_bounds__(kUmThreads, 1) append_umma_kernel(AppendArgs a
             mx8[u] = fmaxf(mx8[u], mx8[u + r]);
           }
         const float mn = mn8[0], mx = mx8[0];
-        const float s32 = __fdiv_rn(__fsub_rn(mx, mn), 3.0f);
+        const float s32 = __fdiv_rn(__fsub_rn(mx, mn), BITS == 4 ? 15.0f : 3.0f);
         const __half s16 = fp16_sat(s32);
         const __half m16 = fp16_sat(mn);
         const float sc = __half2float(s16);
         const float m = __half2float(m16);
         smg[k] = (uint32_t)__half_as_ushort(s16) | ((uint32_t)__half_as_ushort(m16) << 16);
-        if (sc != 0.0f) {
+        if constexpr (BITS == 4) {
+          if (sc != 0.0f) {
+            const float r = __fdiv_rn(1.f, sc);
+#pragma unroll
+            for (int j = GW * k; j < GW * (k + 1); ++j)
+              w[j >> 3] += int4_code_magic(__fsub_rn(v[j], m), r, sc) << (4 * (j & 7));
+#pragma unroll
+            for (int j = GW * k; j < GW * (k + 1); j += 8) w[j >> 3] -= code_magic_sum(8);
+          }
+        } else if (sc != 0.0f) {
           const CodeThresholds th = code_thresholds(sc);
 #pragma unroll
           for (int j = GW * k; j < GW * (k + 1); ++j)
@@ -575,7 +606,18 @@ __global__ void __launch_bounds__(kUmThreads, 1) append_umma_kernel(AppendArgs a
       }
       uint8_t* bp = a.pages + ((size_t)(valid ? blk : 0) * a.hkv + h) * a.bhb;
       const int sl = p & 15;
-      if (kind == 0) {
+      if constexpr (BITS == 4) {
+        if (kind == 0) {
+          if (valid) {
+            uint4* kp = reinterpret_cast<uint4*>(bp + sl * 64);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) kp[j] = make_uint4(w[j], w[4 + j], w[8 + j], w[12 + j]);
+          }
+        } else if (valid) {
+#pragma unroll
+          for (int bb = 0; bb < 64; ++bb) bp[v4_code_offset(sl, bb)] = (uint8_t)(w[bb >> 2] >> (8 * (bb & 3)));
+        }
+      } else if (kind == 0) {
         if (valid) {
           uint4* kp = reinterpret_cast<uint4*>(bp + kKcOff + sl * 32);
           kp[0] = make_uint4(w[0], w[1], w[2], w[3]);
@@ -589,7 +631,7 @@ __global__ void __launch_bounds__(kUmThreads, 1) append_umma_kernel(AppendArgs a
       }
       if (!valid) continue;
 #pragma unroll
-      for (int k = 0; k < NG; ++k) *reinterpret_cast<uint32_t*>(bp + sm_offset(NG, kind, sl, k)) = smg[k];
+      for (int k = 0; k < NG; ++k) *reinterpret_cast<uint32_t*>(bp + sm_offset(NG, kind, sl, k, BITS)) = smg[k];
       __half* wr = window_row(a, slot, h, kind, p, len);
       __half* sr = sink_row(a, slot, h, kind, p);
       if (wr != nullptr || sr != nullptr) {
@@ -666,25 +708,28 @@ okv_status launch_append(const okv_cache_desc* d, const void* k, const void* v, 
   const bool maps = !(flags & OKV_PRE_ROTATED) && T >= kTcMinTokens && rows16 &&
                     encode_tile_map(&map_k, k, d->num_kv_heads, T) && encode_tile_map(&map_v, v, d->num_kv_heads, T);
   if (maps) {
-    const void* kern = a.ng == 1 ? (const void*)append_umma_kernel<1>
-                       : a.ng == 2 ? (const void*)append_umma_kernel<2> : (const void*)append_umma_kernel<4>;
-    static std::atomic<uint32_t> attr_set[3];  // per instantiation: ng = 1, 2, 4 -> 0, 1, 2
-    cudaError_t e = set_smem_limit_once(kern, (int)kUmSmem, attr_set[a.ng >> 1]);
+    using Kernel = void (*)(AppendArgs, int, const CUtensorMap, const CUtensorMap);
+    static const Kernel kernels[2][3] = {
+        {append_umma_kernel<1, 2>, append_umma_kernel<2, 2>, append_umma_kernel<4, 2>},
+        {append_umma_kernel<1, 4>, append_umma_kernel<2, 4>, append_umma_kernel<4, 4>}};
+    const int fi = a.bits == 4, gi = a.ng >> 1;  // ng = 1, 2, 4 -> 0, 1, 2
+    static std::atomic<uint32_t> attr_set[2][3];  // per instantiation
+    cudaError_t e = set_smem_limit_once((const void*)kernels[fi][gi], (int)kUmSmem, attr_set[fi][gi]);
     if (e != cudaSuccess) return fail(OKV_ERR_CUDA, "append smem attribute: %s", cudaGetErrorString(e));
     const int pairs = 2 * d->num_kv_heads;
     const int tiles = (T + kUmTile - 1) / kUmTile;
     const int per_pair = std::max(1, std::min(tiles, device_sm_count() / pairs));
     dim3 grid(per_pair, d->num_kv_heads, 2);
-    switch (a.ng) {
-      case 1: append_umma_kernel<1><<<grid, kUmThreads, kUmSmem, s>>>(a, T, map_k, map_v); break;
-      case 2: append_umma_kernel<2><<<grid, kUmThreads, kUmSmem, s>>>(a, T, map_k, map_v); break;
-      default: append_umma_kernel<4><<<grid, kUmThreads, kUmSmem, s>>>(a, T, map_k, map_v); break;
-    }
+    kernels[fi][gi]<<<grid, kUmThreads, kUmSmem, s>>>(a, T, map_k, map_v);
     return check_launch("append (tcgen05)");
   }
-  if (!(flags & OKV_PRE_ROTATED) && T >= kTcMinTokens) {
-    static std::atomic<uint32_t> attr_set{0};
-    cudaError_t e = set_smem_limit_once((const void*)append_tc_kernel, (int)kTcSmem, attr_set);
+  // append_tc_kernel reads K and V as 32-bit words; rows on odd 2-byte
+  // addresses take the CUDA-core kernel, which reads element by element
+  const bool words4 = (((uintptr_t)k | (uintptr_t)v) & 3u) == 0;
+  if (!(flags & OKV_PRE_ROTATED) && T >= kTcMinTokens && words4) {
+    static std::atomic<uint32_t> attr_set[2];
+    const auto kern = a.bits == 4 ? append_tc_kernel<4> : append_tc_kernel<2>;
+    cudaError_t e = set_smem_limit_once((const void*)kern, (int)kTcSmem, attr_set[a.bits == 4]);
     if (e != cudaSuccess) return fail(OKV_ERR_CUDA, "append smem attribute: %s", cudaGetErrorString(e));
     // about two CTAs per SM over all (KV head, K|V) pairs; each CTA takes whole rounds
     const int pairs = 2 * d->num_kv_heads;
@@ -692,7 +737,7 @@ okv_status launch_append(const okv_cache_desc* d, const void* k, const void* v, 
     const int rounds = (T + kTcRound - 1) / kTcRound;
     const int tokens_per_cta = ((rounds + per_pair - 1) / per_pair) * kTcRound;
     dim3 grid((T + tokens_per_cta - 1) / tokens_per_cta, d->num_kv_heads, 2);
-    append_tc_kernel<<<grid, kTcWarps * 32, kTcSmem, s>>>(a, T, tokens_per_cta);
+    kern<<<grid, kTcWarps * 32, kTcSmem, s>>>(a, T, tokens_per_cta);
     return check_launch("append (tensor cores)");
   }
   dim3 grid((T + kAppTokens - 1) / kAppTokens, d->num_kv_heads, 2);

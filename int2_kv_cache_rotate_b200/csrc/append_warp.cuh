@@ -1,5 +1,5 @@
 // Warp-level append shared by the append kernels and the fused decode-step
-// kernel: rotate (U, Hadamard butterfly, bit-reversal remap), quantise to INT2
+// kernel: rotate (U, Hadamard butterfly, bit-reversal remap), quantise to INT2 or INT4
 // with fp16 scale/min, pack, and write the paged cache and the fp16 rows of
 // the recent-token window and of the sink tokens, for one 32-token tile of
 // one (KV head, K|V).
@@ -7,6 +7,7 @@
 
 #include "okv.h"
 #include "okv_common.cuh"
+#include "okv_internal.h"
 
 namespace okv {
 
@@ -25,8 +26,10 @@ struct AppendArgs {
   float* rotated_out;
   uint32_t* status;
   int hkv, num_blocks, num_slots, mbps, nsink;
-  int ng;   // quantisation groups per vector (128 / group)
-  int bhb;  // bytes of one block-head
+  int ng;    // quantisation groups per vector (128 / group)
+  int bits;  // bits per code: 2 or 4
+  int bhb;   // bytes of one block-head
+  bool pad;  // rows whose slot is -1 are padding: skipped without a flag
   const uint8_t* r_image;  // staged R of every (KV head, K|V) for the tcgen05 append, or null
 };
 
@@ -52,8 +55,10 @@ inline AppendArgs make_append_args(const okv_cache_desc* d, const void* k, const
   a.num_blocks = d->num_blocks;
   a.num_slots = d->num_seq_slots;
   a.mbps = d->max_blocks_per_seq;
-  a.ng = kD / d->group;
-  a.bhb = block_head_bytes(a.ng);
+  a.ng = kD / group_channels(d);
+  a.bits = code_bits(d);
+  a.bhb = block_head_bytes(a.ng, a.bits);
+  a.pad = (d->group & OKV_PAD_ROWS) != 0;
   a.r_image = (const uint8_t*)d->r_image;
   return a;
 }
@@ -81,7 +86,7 @@ __device__ __forceinline__ void finish_token(const AppendArgs& a, int t, int h, 
   const int slot = a.seq_slot[t];
   const int p = a.pos[t];
   if (slot < 0 || slot >= a.num_slots) {
-    if (lane == 0) raise_flag(a.status, OKV_DEV_BAD_SLOT);
+    if (lane == 0 && !(a.pad && slot == -1)) raise_flag(a.status, OKV_DEV_BAD_SLOT);
     return;
   }
   const int len = a.slot_lens[slot];
@@ -99,16 +104,23 @@ __device__ __forceinline__ void finish_token(const AppendArgs& a, int t, int h, 
     float4 o = make_float4(y[0], y[2], y[1], y[3]);
     *reinterpret_cast<float4*>(a.rotated_out + (((size_t)t * 2 + kind) * a.hkv + h) * kD + 4 * r) = o;
   }
-  const Quantized q = quantize_warp(y, a.ng);
+  const Quantized q = a.bits == 4 ? quantize_warp<4>(y, a.ng) : quantize_warp<2>(y, a.ng);
   uint8_t* base = a.pages + ((size_t)blk * a.hkv + h) * a.bhb;
   const int s16 = p & 15;
-  if (kind == 0) {
+  if (a.bits == 4) {
+    if (kind == 0) {
+      *reinterpret_cast<uint16_t*>(base + k4_code_offset(s16, 2 * r)) = (uint16_t)q.byte;
+    } else {
+      base[v4_code_offset(s16, 2 * r)] = (uint8_t)q.byte;
+      base[v4_code_offset(s16, 2 * r + 1)] = (uint8_t)(q.byte >> 8);
+    }
+  } else if (kind == 0) {
     base[kKcOff + s16 * 32 + r] = (uint8_t)q.byte;
   } else {
     base[v_code_offset(s16, r)] = (uint8_t)q.byte;
   }
   // one lane per group (lanes 0 .. ng - 1) writes its group's scale and min
-  if (lane < a.ng) *reinterpret_cast<uint32_t*>(base + sm_offset(a.ng, kind, s16, r * a.ng / 32)) = q.sm;
+  if (lane < a.ng) *reinterpret_cast<uint32_t*>(base + sm_offset(a.ng, kind, s16, r * a.ng / 32, a.bits)) = q.sm;
   __half* wrow = window_row(a, slot, h, kind, p, len);
   __half* srow = sink_row(a, slot, h, kind, p);
   if (wrow != nullptr || srow != nullptr) {

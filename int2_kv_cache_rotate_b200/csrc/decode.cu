@@ -87,7 +87,7 @@ struct DecodeArgs {
   const uint8_t* pages;
   const __half* ring;
   const __half* sink;  // fp16 rows of the first nsink positions
-  float* out;
+  void* out;  // fp32 or bf16 [B][Hq][128]
   uint32_t* status;
   float* qrot;       // [B][Hq][128]
   int8_t* qlimb;     // [B][Hq][2][128]
@@ -98,6 +98,8 @@ struct DecodeArgs {
   float* part;       // [(NC + B)][Hq][kPartStride]
   int batch, hq, hkv, g, nc, num_blocks, num_slots, mbps, nsink;
   int ng;  // quantisation groups per vector (128 / group)
+  int bits;  // bits per code: 2 or 4
+  int out_bf16;
   int hsplit;  // split-K CTAs per cost range: each serves G / hsplit query heads of every KV head
 };
 
@@ -278,7 +280,7 @@ struct WarpState {
 // kWindow: fp16 rows of positions first_row + t of krow0 / vrow0: the window
 // ring (kRing, row = position % W) or the sink rows (row = position);
 // otherwise the INT2 block at blockp.
-template <int G, bool kWindow, bool kRing = true>
+template <int G, int BITS, bool kWindow, bool kRing = true>
 __device__ __forceinline__ void simt_chunk(const DecodeArgs& a, const float* qs /*smem [G][128]*/,
                                            const uint8_t* blockp, const __half* krow0,
                                            const __half* vrow0, int win_first_row, int ntok,
@@ -289,7 +291,23 @@ __device__ __forceinline__ void simt_chunk(const DecodeArgs& a, const float* qs 
 #pragma unroll
   for (int g = 0; g < G; ++g) sc[g] = 0.f;
   if (valid) {
-    if constexpr (!kWindow) {
+    if constexpr (!kWindow && BITS == 4) {
+#pragma unroll
+      for (int wi = 0; wi < 8; ++wi) {
+        // word 8 half + wi: channels 64 half + 8 wi .. + 7, group (8 half + wi) ng / 16
+        const uint32_t w = *reinterpret_cast<const uint32_t*>(blockp + k4_code_offset(tt, 32 * half + 4 * wi));
+        const uint32_t smk =
+            *reinterpret_cast<const uint32_t*>(blockp + sm_offset(a.ng, 0, tt, (8 * half + wi) * a.ng / 16, BITS));
+        const float s = __half2float(__ushort_as_half((unsigned short)(smk & 0xffff)));
+        const float m = __half2float(__ushort_as_half((unsigned short)(smk >> 16)));
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float x = fmaf(s, (float)((w >> (4 * j)) & 15u), m);
+#pragma unroll
+          for (int g = 0; g < G; ++g) sc[g] = fmaf(qs[g * kD + 64 * half + 8 * wi + j], x, sc[g]);
+        }
+      }
+    } else if constexpr (!kWindow) {
       const uint4 w = *reinterpret_cast<const uint4*>(blockp + kKcOff + tt * 32 + 16 * half);
       const uint32_t words[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
@@ -346,12 +364,15 @@ __device__ __forceinline__ void simt_chunk(const DecodeArgs& a, const float* qs 
   for (int t = 0; t < ntok; ++t) {
     float x[4];
     if constexpr (!kWindow) {
-      const uint32_t byte = blockp[v_code_offset(t, lane)];
-      const uint32_t smv = *reinterpret_cast<const uint32_t*>(blockp + sm_offset(a.ng, 1, t, lane * a.ng / 32));
+      uint32_t byte;  // the codes of channels 4 lane .. + 3: one byte, or two
+      if constexpr (BITS == 4)
+        byte = (uint32_t)blockp[v4_code_offset(t, 2 * lane)] | ((uint32_t)blockp[v4_code_offset(t, 2 * lane + 1)] << 8);
+      else byte = blockp[v_code_offset(t, lane)];
+      const uint32_t smv = *reinterpret_cast<const uint32_t*>(blockp + sm_offset(a.ng, 1, t, lane * a.ng / 32, BITS));
       const float s = __half2float(__ushort_as_half((unsigned short)(smv & 0xffff)));
       const float m = __half2float(__ushort_as_half((unsigned short)(smv >> 16)));
 #pragma unroll
-      for (int j = 0; j < 4; ++j) x[j] = fmaf(s, (float)((byte >> (2 * j)) & 3u), m);
+      for (int j = 0; j < 4; ++j) x[j] = fmaf(s, (float)((byte >> (BITS * j)) & ((1u << BITS) - 1u)), m);
     } else {
       const int row = kRing ? (win_first_row + t) % kWin : win_first_row + t;
       const uint2 w = *reinterpret_cast<const uint2*>(vrow0 + (size_t)row * kD + 4 * lane);
@@ -371,7 +392,7 @@ __device__ __forceinline__ void simt_chunk(const DecodeArgs& a, const float* qs 
   }
 }
 
-template <int G>
+template <int G, int BITS>
 __global__ void __launch_bounds__(kDecWarps * 32) decode_simt_kernel(DecodeArgs a) {
   extern __shared__ float smem[];
   float* qs = smem;                               // [G][128]
@@ -421,10 +442,10 @@ __global__ void __launch_bounds__(kDecWarps * 32) decode_simt_kernel(DecodeArgs 
           for (int ci = ci0 + warp; ci < ci1; ci += kDecWarps) {
             if (ci < us.n_wchunk) {  // window positions win_first + 16 ci .. at ring rows pos % W
               const int ntok = min(kBlock, us.n_win - ci * kBlock);
-              simt_chunk<G, true>(a, qs, nullptr, kbase, vbase, us.win_first + ci * kBlock, ntok, st, lane);
+              simt_chunk<G, BITS, true>(a, qs, nullptr, kbase, vbase, us.win_first + ci * kBlock, ntok, st, lane);
             } else {  // sink positions 16 (ci - n_wchunk) .. at sink rows pos
               const int f = (ci - us.n_wchunk) * kBlock;
-              simt_chunk<G, true, false>(a, qs, nullptr, ksink, vsink, f, min(kBlock, us.n_sink - f), st, lane);
+              simt_chunk<G, BITS, true, false>(a, qs, nullptr, ksink, vsink, f, min(kBlock, us.n_sink - f), st, lane);
             }
           }
         }
@@ -436,9 +457,9 @@ __global__ void __launch_bounds__(kDecWarps * 32) decode_simt_kernel(DecodeArgs 
             if (lane == 0) raise_flag(a.status, OKV_DEV_BAD_BLOCK);
             continue;
           }
-          const uint8_t* bp = a.pages + ((size_t)blk * a.hkv + hk) * block_head_bytes(a.ng);
+          const uint8_t* bp = a.pages + ((size_t)blk * a.hkv + hk) * block_head_bytes(a.ng, BITS);
           const int ntok = min(kBlock, us.n_int2 - pi * kBlock);
-          simt_chunk<G, false>(a, qs, bp, nullptr, nullptr, 0, ntok, st, lane);
+          simt_chunk<G, BITS, false>(a, qs, bp, nullptr, nullptr, 0, ntok, st, lane);
         }
       } else if (lane == 0 && warp == 0) {
         raise_flag(a.status, OKV_DEV_BAD_SLOT);
@@ -1788,9 +1809,13 @@ __global__ void __launch_bounds__(kCombThreads) combine_kernel(DecodeArgs a) {
   grid_dep_wait();  // the split partials (and the cost prefix) are read from here on
   const UnitShape sh = unit_shape(clamp_len(a.context_lens, b, a.mbps, a.status, false), a.nsink);
   const long long total = a.prefix[a.batch];
-  float* outp = a.out + ((size_t)b * a.hq + head) * kD;
+  const size_t outp = ((size_t)b * a.hq + head) * kD;
+  auto put = [&](int ch, float x) {
+    if (a.out_bf16) ((__nv_bfloat16*)a.out)[outp + ch] = __float2bfloat16_rn(x);
+    else ((float*)a.out)[outp + ch] = x;
+  };
   if (sh.cost == 0 || total == 0) {
-    if (tid < kD) outp[tid] = 0.f;
+    if (tid < kD) put(tid, 0.f);
     cp_async_wait_all();
     return;
   }
@@ -1907,16 +1932,16 @@ __global__ void __launch_bounds__(kCombThreads) combine_kernel(DecodeArgs a) {
     }
   }
   const float o = part[0] + __shfl_xor_sync(0xffffffffu, part[0], 16);
-  if (lane < 16) outp[16 * warp + lane] = o;
+  if (lane < 16) put(16 * warp + lane, o);
 }
 
-template <int G>
+template <int G, int BITS>
 static okv_status launch_decode_simt(const DecodeArgs& a, cudaStream_t s) {
   const size_t smem = (size_t)(G * kD + kDecWarps * G * kD + kDecWarps * G * 2) * sizeof(float);
   static std::atomic<uint32_t> attr_set{0};
-  cudaError_t e = set_smem_limit_once((const void*)decode_simt_kernel<G>, (int)smem, attr_set);
+  cudaError_t e = set_smem_limit_once((const void*)decode_simt_kernel<G, BITS>, (int)smem, attr_set);
   if (e != cudaSuccess) return fail(OKV_ERR_CUDA, "decode smem attribute: %s", cudaGetErrorString(e));
-  decode_simt_kernel<G><<<a.nc, kDecWarps * 32, smem, s>>>(a);
+  decode_simt_kernel<G, BITS><<<a.nc, kDecWarps * 32, smem, s>>>(a);
   return check_launch("decode");
 }
 
@@ -1934,7 +1959,8 @@ static okv_status launch_decode_heads(const DecodeArgs& a, cudaStream_t s, bool 
   return check_launch("decode");
 }
 
-bool decode_uses_tensor_cores(int g, int hkv, int ng) {
+bool decode_uses_tensor_cores(int g, int hkv, int ng, int bits) {
+  if (bits != 2) return false;
   const bool hkv_ok = hkv == 1 || hkv == 2 || hkv == 4 || hkv == 8;
   return hkv_ok && (ng == 1 || ng == 2 || ng == 4) && (g == 1 || g == 2 || g == 4 || g == 8 || g == 16);
 }
@@ -1943,15 +1969,15 @@ bool decode_uses_tensor_cores(int g, int hkv, int ng) {
 // tensor-core kernel (one at G = 8 with one group per vector, whose CTA holds
 // both n-tiles), with a range split over two (G = 8 grouped) or four (G = 16)
 // CTAs of four query heads; four CTAs per SM for the CUDA-core kernel
-int decode_ranges(int sms, int g, int hkv, int ng) {
-  if (!decode_uses_tensor_cores(g, hkv, ng)) return 4 * sms;
+int decode_ranges(int sms, int g, int hkv, int ng, int bits) {
+  if (!decode_uses_tensor_cores(g, hkv, ng, bits)) return 4 * sms;
   if (g <= 4) return 2 * sms;
   if (g == 8) return sms;
   return sms / 2;  // g = 16
 }
 
 static DecodeArgs make_decode_args(const okv_cache_desc* d, const void* q, int B, const int32_t* seq_slot,
-                                   const int32_t* block_table, const int32_t* context_lens, float* out, void* ws,
+                                   const int32_t* block_table, const int32_t* context_lens, void* out, void* ws,
                                    const DecodePlan& plan) {
   DecodeArgs a;
   a.q = (const __nv_bfloat16*)q;
@@ -1981,7 +2007,9 @@ static DecodeArgs make_decode_args(const okv_cache_desc* d, const void* q, int B
   a.num_blocks = d->num_blocks;
   a.num_slots = d->num_seq_slots;
   a.mbps = d->max_blocks_per_seq;
-  a.ng = kD / d->group;
+  a.ng = kD / group_channels(d);
+  a.bits = code_bits(d);
+  a.out_bf16 = out_bf16(d);
   // grouped layouts at G = 8, and every layout at G = 16: two or four CTAs per
   // cost range, four query heads each
   a.hsplit = a.g == 16 ? 4 : (a.ng > 1 && a.g == 8) ? 2 : 1;
@@ -2008,7 +2036,7 @@ static okv_status launch_decode_tail(const DecodeArgs& a, int B, cudaStream_t s)
   // predecessor; they are left out when the split-K kernel is being timed, so
   // that the events bracket it alone.
   const bool early = ev0 == nullptr;
-  const bool tc = decode_uses_tensor_cores(a.g, a.hkv, a.ng);
+  const bool tc = decode_uses_tensor_cores(a.g, a.hkv, a.ng, a.bits);
   if (tc && a.ng == 2) {
     switch (a.g) {
       case 1: st = launch_decode_heads<1, 2>(a, s, early); break;
@@ -2035,11 +2063,11 @@ static okv_status launch_decode_tail(const DecodeArgs& a, int B, cudaStream_t s)
     }
   } else {
     switch (a.g) {
-      case 1: st = launch_decode_simt<1>(a, s); break;
-      case 2: st = launch_decode_simt<2>(a, s); break;
-      case 4: st = launch_decode_simt<4>(a, s); break;
-      case 8: st = launch_decode_simt<8>(a, s); break;
-      case 16: st = launch_decode_simt<16>(a, s); break;
+      case 1: st = a.bits == 4 ? launch_decode_simt<1, 4>(a, s) : launch_decode_simt<1, 2>(a, s); break;
+      case 2: st = a.bits == 4 ? launch_decode_simt<2, 4>(a, s) : launch_decode_simt<2, 2>(a, s); break;
+      case 4: st = a.bits == 4 ? launch_decode_simt<4, 4>(a, s) : launch_decode_simt<4, 2>(a, s); break;
+      case 8: st = a.bits == 4 ? launch_decode_simt<8, 4>(a, s) : launch_decode_simt<8, 2>(a, s); break;
+      case 16: st = a.bits == 4 ? launch_decode_simt<16, 4>(a, s) : launch_decode_simt<16, 2>(a, s); break;
       default: return fail(OKV_ERR_UNSUPPORTED, "group size %d (Hq/Hkv) not in {1,2,4,8,16}", a.g);
     }
   }
@@ -2055,7 +2083,7 @@ static okv_status launch_decode_tail(const DecodeArgs& a, int B, cudaStream_t s)
 }
 
 okv_status launch_decode(const okv_cache_desc* d, const void* q, int B, const int32_t* seq_slot,
-                         const int32_t* block_table, const int32_t* context_lens, float* out,
+                         const int32_t* block_table, const int32_t* context_lens, void* out,
                          void* ws, const DecodePlan& plan, cudaStream_t s) {
   const DecodeArgs a = make_decode_args(d, q, B, seq_slot, block_table, context_lens, out, ws, plan);
   qrot_kernel<<<B * a.hq, kPrepThreads, 0, s>>>(a);
@@ -2067,7 +2095,7 @@ okv_status launch_decode(const okv_cache_desc* d, const void* q, int B, const in
 okv_status launch_decode_step(const okv_cache_desc* d, const void* k, const void* v, int T, const int32_t* new_slot,
                               const int32_t* new_pos, const int32_t* slot_lens, const void* q, int B,
                               const int32_t* seq_slot, const int32_t* block_table, const int32_t* context_lens,
-                              float* out, void* ws, const DecodePlan& plan, cudaStream_t s) {
+                              void* out, void* ws, const DecodePlan& plan, cudaStream_t s) {
   const DecodeArgs a = make_decode_args(d, q, B, seq_slot, block_table, context_lens, out, ws, plan);
   const AppendArgs aa = make_append_args(d, k, v, new_slot, new_pos, block_table, slot_lens, nullptr);
   const int n_tiles = (T + kAppTokens - 1) / kAppTokens;

@@ -17,10 +17,11 @@ struct DequantArgs {
   const __half* ring;
   const __half* sink;  // fp16 rows of the first nsink positions
   const float* u;  // U of `which`
-  float* out;
+  void* out;  // fp32 or bf16
   uint32_t* status;
   int hkv, num_blocks, num_slots, mbps, max_ctx, which, basis, source, nsink;
-  int ng;  // quantisation groups per vector
+  int ng, bits;  // quantisation groups per vector, bits per code
+  bool bf16, pad;
 };
 
 // grid (ceil(max_ctx/32), Hkv, B), 128 threads; warp w handles tokens w, w+4, ...
@@ -41,7 +42,7 @@ __global__ void __launch_bounds__(128) dequant_kernel(DequantArgs a) {
   }
   const int slot = a.seq_slot[b];
   const bool slot_ok = slot >= 0 && slot < a.num_slots;
-  if (!slot_ok && threadIdx.x == 0 && blockIdx.x == 0 && hk == 0) raise_flag(a.status, OKV_DEV_BAD_SLOT);
+  if (!slot_ok && !(a.pad && slot == -1) && threadIdx.x == 0 && blockIdx.x == 0 && hk == 0) raise_flag(a.status, OKV_DEV_BAD_SLOT);
   const int first_fp16 = (a.source == 1) ? max(0, len - kWin) : len;
   for (int i = warp; i < kTokPerCta; i += 4) {
     const int p = blockIdx.x * kTokPerCta + i;
@@ -62,25 +63,38 @@ __global__ void __launch_bounds__(128) dequant_kernel(DequantArgs a) {
       } else {
         const int blk = a.block_table[(size_t)slot * a.mbps + (p >> 4)];
         if (blk >= 0 && blk < a.num_blocks) {
-          const uint8_t* bp = a.pages + ((size_t)blk * a.hkv + hk) * block_head_bytes(a.ng);
+          const uint8_t* bp = a.pages + ((size_t)blk * a.hkv + hk) * block_head_bytes(a.ng, a.bits);
           const int t = p & 15;
-          const uint32_t byte = a.which == 0 ? bp[kKcOff + t * 32 + lane] : bp[v_code_offset(t, lane)];
+          // the codes of channels 4 lane .. 4 lane + 3: one byte, or two
+          uint32_t byte;
+          if (a.bits == 4)
+            byte = a.which == 0 ? (uint32_t)*reinterpret_cast<const uint16_t*>(bp + k4_code_offset(t, 2 * lane))
+                                : (uint32_t)bp[v4_code_offset(t, 2 * lane)] |
+                                      ((uint32_t)bp[v4_code_offset(t, 2 * lane + 1)] << 8);
+          else
+            byte = a.which == 0 ? bp[kKcOff + t * 32 + lane] : bp[v_code_offset(t, lane)];
           // channels 4 lane .. 4 lane + 3 lie in group 4 lane / group = lane ng / 32
           const uint32_t sm =
-              *reinterpret_cast<const uint32_t*>(bp + sm_offset(a.ng, a.which, t, lane * a.ng / 32));
+              *reinterpret_cast<const uint32_t*>(bp + sm_offset(a.ng, a.which, t, lane * a.ng / 32, a.bits));
           const float s = __half2float(__ushort_as_half((unsigned short)(sm & 0xffff)));
           const float m = __half2float(__ushort_as_half((unsigned short)(sm >> 16)));
 #pragma unroll
-          for (int j = 0; j < 4; ++j) z[j] = fmaf(s, (float)((byte >> (2 * j)) & 3u), m);
+          for (int j = 0; j < 4; ++j) z[j] = fmaf(s, (float)((byte >> (a.bits * j)) & ((1u << a.bits) - 1u)), m);
           have = true;
         } else if (lane == 0) {
           raise_flag(a.status, OKV_DEV_BAD_BLOCK);
         }
       }
     }
-    float* dst = a.out + (((size_t)b * a.hkv + hk) * a.max_ctx + p) * kD;
+    const size_t dst = (((size_t)b * a.hkv + hk) * a.max_ctx + p) * kD;
     if (a.basis == 0 || !have) {
-      *reinterpret_cast<float4*>(dst + 4 * lane) = make_float4(z[0], z[1], z[2], z[3]);
+      if (a.bf16) {
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(z[0], z[1]), hi = __floats2bfloat162_rn(z[2], z[3]);
+        *reinterpret_cast<uint2*>((__nv_bfloat16*)a.out + dst + 4 * lane) =
+            make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+      } else {
+        *reinterpret_cast<float4*>((float*)a.out + dst + 4 * lane) = make_float4(z[0], z[1], z[2], z[3]);
+      }
       continue;
     }
     // back to the original basis: y_i = z_br(i), x = y H, out_c = sum_i x_i U[c][i]
@@ -98,7 +112,10 @@ __global__ void __launch_bounds__(128) dequant_kernel(DequantArgs a) {
       for (int j = 0; j < 4; ++j) o[j] = fmaf(xi, us_[(lane + 32 * j) * kUPadDq + i], o[j]);
     }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) dst[lane + 32 * j] = o[j];
+    for (int j = 0; j < 4; ++j) {
+      if (a.bf16) ((__nv_bfloat16*)a.out)[dst + lane + 32 * j] = __float2bfloat16_rn(o[j]);
+      else ((float*)a.out)[dst + lane + 32 * j] = o[j];
+    }
   }
 }
 
@@ -106,7 +123,7 @@ __global__ void __launch_bounds__(128) dequant_kernel(DequantArgs a) {
 
 okv_status launch_dequant(const okv_cache_desc* d, int B, const int32_t* seq_slot,
                           const int32_t* block_table, const int32_t* context_lens, int max_ctx,
-                          int which, int basis, int source, float* out, cudaStream_t s) {
+                          int which, int basis, int source, void* out, cudaStream_t s) {
   DequantArgs a;
   a.seq_slot = seq_slot;
   a.block_table = block_table;
@@ -122,7 +139,10 @@ okv_status launch_dequant(const okv_cache_desc* d, int B, const int32_t* seq_slo
   a.num_blocks = d->num_blocks;
   a.num_slots = d->num_seq_slots;
   a.mbps = d->max_blocks_per_seq;
-  a.ng = kD / d->group;
+  a.ng = kD / group_channels(d);
+  a.bits = code_bits(d);
+  a.bf16 = out_bf16(d);
+  a.pad = (d->group & OKV_PAD_ROWS) != 0;
   a.max_ctx = max_ctx;
   a.which = which;
   a.basis = basis;

@@ -49,7 +49,7 @@ using namespace okv;
 
 extern "C" okv_status okv_decode_attention_noalloc(const okv_cache_desc* desc, const void* q, int32_t B,
                                                    const int32_t* seq_slot, const int32_t* block_table,
-                                                   const int32_t* context_lens, float* out, void* stream) {
+                                                   const int32_t* context_lens, void* out, void* stream) {
   okv_status st = validate_desc(desc);
   if (st != OKV_OK) return st;
   if (B < 0) return fail(OKV_ERR_INVALID_ARG, "B must be >= 0");
@@ -61,7 +61,8 @@ extern "C" okv_status okv_decode_attention_noalloc(const okv_cache_desc* desc, c
     return fail(OKV_ERR_UNSUPPORTED, "Hq/Hkv = %d not in {1,2,4,8,16}", g);
   if ((long long)B * desc->num_kv_heads * ((long long)desc->max_blocks_per_seq + kWinCost) >= 0x7fffffffLL)
     return fail(OKV_ERR_INVALID_ARG, "B * Hkv * max_blocks_per_seq too large");
-  const DecodePlan plan = make_decode_plan(B, desc->num_q_heads, desc->num_kv_heads, kD / desc->group);
+  if ((uintptr_t)out % (out_bf16(desc) ? 2 : 4)) return fail(OKV_ERR_INVALID_ARG, "out must be element aligned");
+  const DecodePlan plan = make_decode_plan(B, desc->num_q_heads, desc->num_kv_heads, kD / group_channels(desc), code_bits(desc));
   if (plan.total > (size_t)OKV_NOALLOC_SCRATCH_BYTES)
     return fail(OKV_ERR_INVALID_ARG,
                 "batch too large for the built-in scratch: needs %zu bytes, the static array holds %zu "

@@ -63,10 +63,12 @@ static bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
 okv_status validate_desc(const okv_cache_desc* d) {
   if (d == nullptr) return fail(OKV_ERR_INVALID_ARG, "desc is NULL");
+  const int group = group_channels(d);
   if (d->head_dim != kD || d->block_tokens != kBlock || d->window != kWin ||
-      (d->group != 32 && d->group != 64 && d->group != 128))
-    return fail(OKV_ERR_UNSUPPORTED, "only head_dim=128, group in {32, 64, 128}, block_tokens=16, window=128 "
-                "are built (got %d, %d, %d, %d)", d->head_dim, d->group, d->block_tokens, d->window);
+      (group != 32 && group != 64 && group != 128))
+    return fail(OKV_ERR_UNSUPPORTED, "only head_dim=128, group in {32, 64, 128} (with format bits of 0x%x), "
+                "block_tokens=16, window=128 are built (got %d, %d, %d, %d)", kFormatBits, d->head_dim, d->group,
+                d->block_tokens, d->window);
   if (d->num_kv_heads < 1 || d->num_q_heads < 1 || d->num_q_heads % d->num_kv_heads != 0)
     return fail(OKV_ERR_INVALID_ARG, "num_q_heads (%d) must be a positive multiple of num_kv_heads (%d)",
                 d->num_q_heads, d->num_kv_heads);
@@ -92,14 +94,14 @@ okv_status validate_desc(const okv_cache_desc* d) {
 
 static size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
-DecodePlan make_decode_plan(int batch, int hq, int hkv, int ng) {
+DecodePlan make_decode_plan(int batch, int hq, int hkv, int ng, int bits) {
   DecodePlan p;
   p.batch = batch;
   p.hq = hq;
   p.hkv = hkv;
   p.g = hq / hkv;
   const int sms = device_sm_count();
-  p.num_ctas = decode_ranges(sms > 0 ? sms : 148, p.g, hkv, ng);
+  p.num_ctas = decode_ranges(sms > 0 ? sms : 148, p.g, hkv, ng, bits);
   if (p.num_ctas > 1024) p.num_ctas = 1024;  // the combine caches one weight per split
   p.num_units = batch * hkv;
   size_t off = 0;
@@ -125,7 +127,7 @@ using namespace okv;
 
 extern "C" {
 
-int32_t okv_version(void) { return 3; }
+int32_t okv_version(void) { return 4; }
 
 okv_status okv_time_next_decode_kernel(void* start_event, void* stop_event) {
   if ((start_event == nullptr) != (stop_event == nullptr))
@@ -150,8 +152,9 @@ const char* okv_status_string(okv_status s) {
 }
 
 size_t okv_block_head_bytes(int32_t group) {
-  if (group != 32 && group != 64 && group != 128) return 0;
-  return (size_t)block_head_bytes(kD / group);
+  const int channels = group & ~kFormatBits;
+  if (channels != 32 && channels != 64 && channels != 128) return 0;
+  return (size_t)block_head_bytes(kD / channels, (group & OKV_INT4) ? 4 : 2);
 }
 
 size_t okv_pages_bytes(int32_t num_blocks, int32_t num_kv_heads, int32_t group) {
@@ -208,7 +211,7 @@ size_t okv_prefill_workspace_bytes(const okv_cache_desc* desc, int32_t T) {
 }
 
 okv_status okv_prefill_attention(const okv_cache_desc* desc, const void* q, int32_t T, int32_t slot,
-                                 int32_t context_len, const int32_t* block_table, float* out, void* workspace,
+                                 int32_t context_len, const int32_t* block_table, void* out, void* workspace,
                                  size_t workspace_bytes, void* stream) {
   okv_status st = validate_desc(desc);
   if (st != OKV_OK) return st;
@@ -222,8 +225,8 @@ okv_status okv_prefill_attention(const okv_cache_desc* desc, const void* q, int3
     return fail(OKV_ERR_INVALID_ARG, "context_len %d must be in [T = %d, %lld]", context_len, T,
                 (long long)desc->max_blocks_per_seq * kBlock);
   if ((long long)T * desc->num_q_heads > 0x7fffffffLL) return fail(OKV_ERR_INVALID_ARG, "T * Hq too large");
-  if ((uintptr_t)q % 2 || (uintptr_t)out % 4 || (uintptr_t)workspace % 256)
-    return fail(OKV_ERR_INVALID_ARG, "q must be 2-byte, out 4-byte and workspace 256-byte aligned");
+  if ((uintptr_t)q % 16 || (uintptr_t)out % (out_bf16(desc) ? 2 : 4) || (uintptr_t)workspace % 256)
+    return fail(OKV_ERR_INVALID_ARG, "q must be 16-byte, out element and workspace 256-byte aligned");
   const size_t need = prefill_workspace_bytes(T, desc->num_q_heads);
   if (workspace_bytes < need)
     return fail(OKV_ERR_INVALID_ARG, "workspace too small: %zu < %zu bytes", workspace_bytes, need);
@@ -232,12 +235,12 @@ okv_status okv_prefill_attention(const okv_cache_desc* desc, const void* q, int3
 
 size_t okv_decode_workspace_bytes(const okv_cache_desc* desc, int32_t B) {
   if (validate_desc(desc) != OKV_OK || B < 0) return 0;
-  return make_decode_plan(B, desc->num_q_heads, desc->num_kv_heads, kD / desc->group).total;
+  return make_decode_plan(B, desc->num_q_heads, desc->num_kv_heads, kD / group_channels(desc), code_bits(desc)).total;
 }
 
 okv_status okv_decode_attention(const okv_cache_desc* desc, const void* q, int32_t B,
                                 const int32_t* seq_slot, const int32_t* block_table,
-                                const int32_t* context_lens, float* out, void* workspace,
+                                const int32_t* context_lens, void* out, void* workspace,
                                 size_t workspace_bytes, void* stream) {
   okv_status st = validate_desc(desc);
   if (st != OKV_OK) return st;
@@ -250,8 +253,9 @@ okv_status okv_decode_attention(const okv_cache_desc* desc, const void* q, int32
     return fail(OKV_ERR_UNSUPPORTED, "Hq/Hkv = %d not in {1,2,4,8,16}", g);
   if ((long long)B * desc->num_kv_heads * ((long long)desc->max_blocks_per_seq + kWinCost) >= 0x7fffffffLL)
     return fail(OKV_ERR_INVALID_ARG, "B * Hkv * max_blocks_per_seq too large");
-  if ((uintptr_t)workspace % 256) return fail(OKV_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
-  const DecodePlan plan = make_decode_plan(B, desc->num_q_heads, desc->num_kv_heads, kD / desc->group);
+  if ((uintptr_t)workspace % 256 || (uintptr_t)out % (out_bf16(desc) ? 2 : 4))
+    return fail(OKV_ERR_INVALID_ARG, "workspace must be 256-byte and out element aligned");
+  const DecodePlan plan = make_decode_plan(B, desc->num_q_heads, desc->num_kv_heads, kD / group_channels(desc), code_bits(desc));
   if (workspace_bytes < plan.total)
     return fail(OKV_ERR_INVALID_ARG, "workspace too small: %zu < %zu bytes", workspace_bytes, plan.total);
   return launch_decode(desc, q, B, seq_slot, block_table, context_lens, out, workspace, plan,
@@ -261,7 +265,7 @@ okv_status okv_decode_attention(const okv_cache_desc* desc, const void* q, int32
 okv_status okv_decode_step(const okv_cache_desc* desc, const void* k, const void* v, int32_t T,
                            const int32_t* new_seq_slot, const int32_t* new_pos, const int32_t* slot_lens,
                            const void* q, int32_t B, const int32_t* seq_slot, const int32_t* block_table,
-                           const int32_t* context_lens, float* out, void* workspace, size_t workspace_bytes,
+                           const int32_t* context_lens, void* out, void* workspace, size_t workspace_bytes,
                            void* stream) {
   okv_status st = validate_desc(desc);
   if (st != OKV_OK) return st;
@@ -281,8 +285,9 @@ okv_status okv_decode_step(const okv_cache_desc* desc, const void* k, const void
     return fail(OKV_ERR_UNSUPPORTED, "Hq/Hkv = %d not in {1,2,4,8,16}", g);
   if ((long long)B * desc->num_kv_heads * ((long long)desc->max_blocks_per_seq + kWinCost) >= 0x7fffffffLL)
     return fail(OKV_ERR_INVALID_ARG, "B * Hkv * max_blocks_per_seq too large");
-  if ((uintptr_t)workspace % 256) return fail(OKV_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
-  const DecodePlan plan = make_decode_plan(B, desc->num_q_heads, desc->num_kv_heads, kD / desc->group);
+  if ((uintptr_t)workspace % 256 || (uintptr_t)out % (out_bf16(desc) ? 2 : 4))
+    return fail(OKV_ERR_INVALID_ARG, "workspace must be 256-byte and out element aligned");
+  const DecodePlan plan = make_decode_plan(B, desc->num_q_heads, desc->num_kv_heads, kD / group_channels(desc), code_bits(desc));
   if (workspace_bytes < plan.total)
     return fail(OKV_ERR_INVALID_ARG, "workspace too small: %zu < %zu bytes", workspace_bytes, plan.total);
   const cudaStream_t s = (cudaStream_t)stream;
@@ -298,7 +303,7 @@ okv_status okv_decode_step(const okv_cache_desc* desc, const void* k, const void
 okv_status okv_dequantize(const okv_cache_desc* desc, int32_t B, const int32_t* seq_slot,
                           const int32_t* block_table, const int32_t* context_lens,
                           int32_t max_ctx, int32_t which, int32_t basis, int32_t source,
-                          float* out, void* stream) {
+                          void* out, void* stream) {
   okv_status st = validate_desc(desc);
   if (st != OKV_OK) return st;
   if (B < 0 || max_ctx < 0) return fail(OKV_ERR_INVALID_ARG, "B and max_ctx must be >= 0");

@@ -27,6 +27,27 @@ __host__ __device__ __forceinline__ int block_head_bytes(int ng) { return 1024 +
 __host__ __device__ __forceinline__ int sm_offset(int ng, int kind, int t, int k) {
   return 1024 + 64 * ng * kind + 4 * (t * ng + k);
 }
+// The same for codes of `bits` = 2 or 4 bits: K codes from 0, V codes from
+// 256 bits, then the pairs from 512 bits.
+__host__ __device__ __forceinline__ int block_head_bytes(int ng, int bits) { return 512 * bits + 128 * ng; }
+__host__ __device__ __forceinline__ int sm_offset(int ng, int kind, int t, int k, int bits) {
+  return 512 * bits + 64 * ng * kind + 4 * (t * ng + k);
+}
+// Byte offsets of canonical code byte b (channels 2b, 2b + 1) of token t in a
+// 4-bit block-head.  K: word w = b >> 2 of the row sits at word 4 (w & 3) +
+// (w >> 2), so that the 16 bytes a lane quad t reads of a row are words t, 4 +
+// t, 8 + t, 12 + t: word 4 s + t goes to score MMA s, which then covers
+// channels 32 s .. 32 s + 31 only, and one code order serves every group size.
+// V: 16-byte chunk (b & 7, t >> 2) of half b >> 5 holds bytes b, 8 + b, 16 +
+// b, 24 + b of four tokens, one 32-bit word per byte, so that word m of a lane
+// is the A operand of m-tile m, channels 16 m .. 16 m + 15.
+constexpr int kVcOff4 = 1024;
+__host__ __device__ __forceinline__ int k4_code_offset(int t, int b) {
+  return t * 64 + ((b >> 2) & 3) * 16 + (b >> 4) * 4 + (b & 3);
+}
+__host__ __device__ __forceinline__ int v4_code_offset(int t, int b) {
+  return kVcOff4 + (b >> 5) * 512 + (((b & 7) * 4 + (t >> 2)) << 4) + ((b >> 3) & 3) * 4 + (t & 3);
+}
 constexpr float kInvSqrtD = 0.088388347648318440550f;  // 1/sqrt(128)
 constexpr float kLog2e = 1.4426950408889634074f;
 
@@ -129,18 +150,50 @@ __device__ __forceinline__ uint32_t int2_code_neg(float x, const CodeThresholds&
   return a + b + c;
 }
 
+// The 4-bit code of x = fl(z - m) for an fp16 scale s > 0,
+// clamp(rint_even(fl(x / s)), 0, 15), without a division per value.  The
+// argument above holds for every half-integer h = k + 1/2 up to 29/2: fl(x / s)
+// meets h within half an ulp of h, (2^j / h) 2^-24 relative for h in [2^j,
+// 2^(j+1)), while neighbouring fp32 numbers of h s (exact: 5 + 11 bits) lie
+// more than 2^-24 away; ties go to the even code.  So the code is at least
+// k + 1 exactly where x > h s (k even) or x >= h s (k odd), and only the
+// half-integer nearest to x / s needs the exact comparison: with r = 1 / s
+// rounded, k = rint(x r - 1/2) clamped to [0, 14] has x / s in (k - 1/4, k +
+// 5/4) or beyond the ends, so every other decision is settled.  x >= h s is
+// x > the predecessor of h s, one less in its bits.  NaN gives 0.
+// Returns 0x4B400000 + code (the magic number's bits stay in, so that a caller
+// sums several codes with shifts and takes one constant off).
+constexpr uint32_t kCodeMagicBits = 0x4B400000u;  // 1.5 * 2^23
+__device__ __forceinline__ uint32_t int4_code_magic(float x, float r, float s) {
+  const float t = fminf(fmaxf(fmaf(x, r, -0.5f), 0.f), 14.f);
+  const float km = t + 12582912.f;
+  const uint32_t kb = __float_as_uint(km);
+  const float thr = fmaf(km - 12582912.f, s, 0.5f * s);
+  uint32_t up;
+  asm("set.gt.u32.f32 %0, %1, %2;" : "=r"(up) : "f"(x), "f"(__uint_as_float(__float_as_uint(thr) - (kb & 1u))));
+  return kb - up;  // up = -1 where the code is k + 1
+}
+// What n codes of a word leave behind: sum of kCodeMagicBits << 4 i, i = 0 .. n - 1, mod 2^32
+__host__ __device__ constexpr uint32_t code_magic_sum(int n) {
+  uint32_t x = 0;
+  for (int i = 0; i < n; ++i) x += kCodeMagicBits << (4 * i);
+  return x;
+}
+
 // INT2 group quantiser over the 128 values of a warp (y[a] = value at
 // pre-permutation index l + 32a, i.e. rotated channel 4*rev5(l) + rev2(a)).
 // With ng groups per vector (ng = 128 / group: 1, 2 or 4), the group of
 // lane l's four channels is rev5(l) * ng / 32: the lanes that share
 // l mod ng form one group, so the min/max reductions stop at lane distance
 // ng.  All steps are IEEE fp32 round-to-nearest; returns this lane's packed
-// code byte (canonical byte rev5(l)) and its group's fp16 scale/min bits.
+// code byte (canonical byte rev5(l); with 4 bits, bytes 2 rev5(l) and + 1) and
+// its group's fp16 scale/min bits.
 struct Quantized {
   uint32_t byte;
   uint32_t sm;  // fp16 scale in bits 0-15, fp16 min in bits 16-31
 };
 
+template <int BITS = 2>
 __device__ __forceinline__ Quantized quantize_warp(const float y[4], int ng = 1) {
   float mn = fminf(fminf(y[0], y[1]), fminf(y[2], y[3]));
   float mx = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]));
@@ -150,13 +203,20 @@ __device__ __forceinline__ Quantized quantize_warp(const float y[4], int ng = 1)
     mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
   }
-  const float s32 = __fdiv_rn(__fsub_rn(mx, mn), 3.0f);
+  const float s32 = __fdiv_rn(__fsub_rn(mx, mn), BITS == 4 ? 15.0f : 3.0f);
   const __half s16 = fp16_sat(s32);
   const __half m16 = fp16_sat(mn);
   const float s = __half2float(s16);
   const float m = __half2float(m16);
   uint32_t byte = 0;
-  if (s != 0.0f) {
+  if constexpr (BITS == 4) {
+    if (s != 0.0f) {
+      const float r = __fdiv_rn(1.f, s);
+#pragma unroll
+      for (int a = 0; a < 4; ++a) byte += int4_code_magic(__fsub_rn(y[a], m), r, s) << (4 * rev2(a));
+      byte -= code_magic_sum(4);
+    }
+  } else if (s != 0.0f) {
     const CodeThresholds th = code_thresholds(s);
 #pragma unroll
     for (int a = 0; a < 4; ++a) byte -= int2_code_neg(__fsub_rn(y[a], m), th) << (2 * rev2(a));

@@ -16,6 +16,12 @@ okv_status check_launch(const char* what);
 okv_status validate_desc(const okv_cache_desc* d);
 int device_sm_count();
 
+// the parts of okv_cache_desc.group
+constexpr int kFormatBits = OKV_INT4 | OKV_OUT_BF16 | OKV_PAD_ROWS;
+inline int group_channels(const okv_cache_desc* d) { return d->group & ~kFormatBits; }
+inline int code_bits(const okv_cache_desc* d) { return (d->group & OKV_INT4) ? 4 : 2; }
+inline bool out_bf16(const okv_cache_desc* d) { return (d->group & OKV_OUT_BF16) != 0; }
+
 // Sets a kernel's dynamic shared-memory limit once per device (bit d of
 // `done` records device d < 32; higher ordinals set it on every call).  The
 // attribute belongs to the device's context, so a context reset would need
@@ -61,10 +67,10 @@ constexpr int kQsStride = 8;      // floats per query head in the query-scale wo
 constexpr int kWinCost = 4;       // cost of one 16-row fp16 chunk in block units (all heads)
 constexpr int kFusedAppendMaxTokens = 127;  // okv_decode_step fuses appends this short with the query rotation
 // split-K kernel choice and residency (decode.cu)
-bool decode_uses_tensor_cores(int g, int hkv, int ng);
-int decode_ranges(int sms, int g, int hkv, int ng);
+bool decode_uses_tensor_cores(int g, int hkv, int ng, int bits);
+int decode_ranges(int sms, int g, int hkv, int ng, int bits);
 
-DecodePlan make_decode_plan(int batch, int hq, int hkv, int ng);
+DecodePlan make_decode_plan(int batch, int hq, int hkv, int ng, int bits);
 
 // bytes of one (KV head, K|V) staged R in the cache's image buffer: three bf16
 // parts x 128 x 128
@@ -77,17 +83,17 @@ okv_status launch_append(const okv_cache_desc* d, const void* k, const void* v, 
                          const int32_t* slot_lens, uint32_t flags, float* rotated_out,
                          cudaStream_t s);
 okv_status launch_decode(const okv_cache_desc* d, const void* q, int B, const int32_t* seq_slot,
-                         const int32_t* block_table, const int32_t* context_lens, float* out,
+                         const int32_t* block_table, const int32_t* context_lens, void* out,
                          void* ws, const DecodePlan& plan, cudaStream_t s);
 okv_status launch_decode_step(const okv_cache_desc* d, const void* k, const void* v, int T, const int32_t* new_slot,
                               const int32_t* new_pos, const int32_t* slot_lens, const void* q, int B,
                               const int32_t* seq_slot, const int32_t* block_table, const int32_t* context_lens,
-                              float* out, void* ws, const DecodePlan& plan, cudaStream_t s);
+                              void* out, void* ws, const DecodePlan& plan, cudaStream_t s);
 okv_status launch_prefill(const okv_cache_desc* d, const void* q, int T, int slot, int context_len,
-                          const int32_t* block_table, float* out, void* ws, cudaStream_t s);
+                          const int32_t* block_table, void* out, void* ws, cudaStream_t s);
 size_t prefill_workspace_bytes(int T, int hq);
 okv_status launch_dequant(const okv_cache_desc* d, int B, const int32_t* seq_slot,
                           const int32_t* block_table, const int32_t* context_lens, int max_ctx,
-                          int which, int basis, int source, float* out, cudaStream_t s);
+                          int which, int basis, int source, void* out, cudaStream_t s);
 
 }  // namespace okv

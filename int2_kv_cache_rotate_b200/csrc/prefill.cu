@@ -45,7 +45,8 @@ struct PrefillArgs {
   __half* qlo;   // [T][Hq][128]: lo half
   float* qaux;   // [T][Hq][8]: sum of q~ per group (4), 2^e, spare
   float* obuf;   // [T][Hq][132]: o' (128), l, spare
-  float* out;    // [T][Hq][128]
+  void* out;     // [T][Hq][128], fp32 or bf16
+  int out_bf16;
   int T, hq, hkv, g, ng, bhb, slot, L, first, mbps, num_blocks, nsink;
 };
 
@@ -290,6 +291,27 @@ __device__ __forceinline__ uint32_t codes_at_bit1(uint32_t x) {
     return x >> (2 * k - 1);
 }
 
+// The same for 4-bit codes: (1024 + lo, 1024 + hi) - 1024 for codes at bits
+// 0-3 and 16-19, and centred as 2 c - 15 with half the scale, s c + m = (s /
+// 2)(2 c - 15) + (m + 7.5 s), for codes at bits 1-4 and 17-20.
+__device__ __forceinline__ uint32_t codes4_to_half2(uint32_t x) {
+  const uint32_t b = (x & 0x000F000Fu) | kF16Bias2, bias = kF16Bias2;
+  const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&b), *reinterpret_cast<const __half2*>(&bias));
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+constexpr uint32_t kF16Centre4 = 0x640F640Fu;  // (1039, 1039)
+__device__ __forceinline__ uint32_t centred4_to_half2(uint32_t x) {
+  const uint32_t b = (x & 0x001E001Eu) | kF16Bias2, bias = kF16Centre4;
+  const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&b), *reinterpret_cast<const __half2*>(&bias));
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+// the 8 key codes of a word (channel 2 b + k at bits 8 b + 4 k) as 4 fp16 pairs of adjacent channels
+__device__ __forceinline__ uint4 word4_to_half2x4(uint32_t w) {
+  const uint32_t hi = w >> 4;
+  return make_uint4(codes4_to_half2(__byte_perm(w, hi, 0x4400u)), codes4_to_half2(__byte_perm(w, hi, 0x5511u)),
+                    codes4_to_half2(__byte_perm(w, hi, 0x6622u)), codes4_to_half2(__byte_perm(w, hi, 0x7733u)));
+}
+
 // 16 consecutive-channel codes of one word (channel 4 b + k at bits 8 b + 2 k)
 // as 8 fp16 pairs of adjacent channels (centred: 2 c - 3)
 template <bool kCentred>
@@ -316,7 +338,7 @@ __device__ __forceinline__ float ex2_ftz(float x) {
   return y;
 }
 
-template <int NG>
+template <int NG, int BITS>
 __global__ void __launch_bounds__(kUpThreads, 1) prefill_umma_kernel(PrefillArgs a) {
   static_assert(NG == 1 || NG == 2 || NG == 4, "one, two or four quantisation groups per vector");
   constexpr int kSW = 64 * NG;                  // score columns per buffer
@@ -388,15 +410,19 @@ __global__ void __launch_bounds__(kUpThreads, 1) prefill_umma_kernel(PrefillArgs
   // ---- staging: per-thread roles and the register-held fetch of one chunk
   const int stid = tid - 32 * kUpSmxWarps, sw = stid >> 5;
   const int ktk = 16 * sw + (lane & 15), kkb = lane >> 4;      // key token, K-block (64 channels)
-  const int vtq = lane & 15, vbq = 2 * sw + (lane >> 4);       // value token quad, channel sixteen
+  // value token quad, and the 16 channels this thread stages of it: with 2-bit
+  // codes the sixteen 16 vbq .. + 15, with 4-bit codes channels 16 j + 2 vbq, + 1
+  // of every 16-channel tile j (the two 16-byte chunks of the quad's byte vbq)
+  const int vtq = lane & 15, vbq = BITS == 4 ? sw + 4 * (lane >> 4) : 2 * sw + (lane >> 4);
+  auto vchan = [&](int j) { return BITS == 4 ? 16 * j + 2 * vbq : 16 * vbq + 2 * j; };  // channel of pair j = 0 .. 7
   // What a staging thread fetched of one chunk, held in registers until it is
   // staged; two of them alternate, so that a chunk's loads are in flight two
   // chunks before its tiles are written.
   struct Fetched {
     int ksrc, vsrc[4], sbad;  // sources: 0 masked, 1 INT2, 2 fp16; sbad: a block id was out of range
     int p0;                   // first position of the chunk
-    uint4 kr0;                // INT2 key codes of the token (64 channels)
-    uint4 vw;                 // INT2 value codes of the quad (16 channels x 4 tokens)
+    uint4 kr[BITS / 2];       // key codes of the token (64 channels; 4 bits: words j, then words 4 + j)
+    uint4 vw[BITS / 2];       // value codes of the quad (16 channels x 4 tokens)
     uint32_t ksmw[NG];        // the token's (scale, min) per group: key scales for kkb 0, value scales for kkb 1
   };
   Fetched fa, fb;
@@ -428,6 +454,31 @@ __global__ void __launch_bounds__(kUpThreads, 1) prefill_umma_kernel(PrefillArgs
     *bp = a.pages + ((size_t)blk * a.hkv + hk) * a.bhb;
     return 1;
   };
+  // codes of key token t16 and (scale, min) pairs of token t16, and value codes, from block-head bp
+  auto fetch_k = [&](Fetched& f, const uint8_t* bp, int t16) {
+    if constexpr (BITS == 4) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint2 x = *reinterpret_cast<const uint2*>(bp + t16 * 64 + 16 * j + 8 * kkb);
+        (&f.kr[0].x)[j] = x.x;
+        (&f.kr[BITS / 2 - 1].x)[j] = x.y;
+      }
+    } else {
+      f.kr[0] = *reinterpret_cast<const uint4*>(bp + kKcOff + t16 * 32 + 16 * kkb);
+    }
+#pragma unroll
+    for (int k = 0; k < NG; ++k) f.ksmw[k] = *reinterpret_cast<const uint32_t*>(bp + sm_offset(NG, kkb, t16, k, BITS));
+  };
+  auto fetch_v = [&](Fetched& f, const uint8_t* bp) {
+    if constexpr (BITS == 4) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        f.vw[i * (BITS / 2 - 1)] =
+            *reinterpret_cast<const uint4*>(bp + kVcOff4 + 512 * i + ((vbq * 4 + (vtq & 3)) << 4));
+    } else {
+      f.vw[0] = *reinterpret_cast<const uint4*>(bp + kVcOff + ((vbq * 4 + (vtq & 3)) << 4));
+    }
+  };
   auto fetch = [&](Fetched& f, int c, int kblk, int vblk) {
     const int p0 = kUpKC * c;
     f.p0 = p0;
@@ -441,30 +492,17 @@ __global__ void __launch_bounds__(kUpThreads, 1) prefill_umma_kernel(PrefillArgs
         f.sbad = 1;
       }
       f.ksrc = kok ? 1 : 0;
-      if (kok) {
-        const uint8_t* bp = a.pages + ((size_t)kblk * a.hkv + hk) * a.bhb;
-        f.kr0 = *reinterpret_cast<const uint4*>(bp + kKcOff + (ktk & 15) * 32 + 16 * kkb);
-#pragma unroll
-        for (int k = 0; k < NG; ++k)
-          f.ksmw[k] = *reinterpret_cast<const uint32_t*>(bp + sm_offset(NG, kkb, ktk & 15, k));
-      }
+      if (kok) fetch_k(f, a.pages + ((size_t)kblk * a.hkv + hk) * a.bhb, ktk & 15);
 #pragma unroll
       for (int i = 0; i < 4; ++i) f.vsrc[i] = vok ? 1 : 0;
-      if (vok)
-        f.vw = *reinterpret_cast<const uint4*>(a.pages + ((size_t)vblk * a.hkv + hk) * a.bhb + kVcOff +
-                                               ((vbq * 4 + (vtq & 3)) << 4));
+      if (vok) fetch_v(f, a.pages + ((size_t)vblk * a.hkv + hk) * a.bhb);
       return;
     }
     {
       const uint8_t* bp = nullptr;
       const int p = p0 + ktk;
       f.ksrc = locate(f, p, kblk, &bp);
-      if (f.ksrc == 1) {
-        f.kr0 = *reinterpret_cast<const uint4*>(bp + kKcOff + (p & 15) * 32 + 16 * kkb);
-#pragma unroll
-        for (int k = 0; k < NG; ++k)
-          f.ksmw[k] = *reinterpret_cast<const uint32_t*>(bp + sm_offset(NG, kkb, p & 15, k));
-      }
+      if (f.ksrc == 1) fetch_k(f, bp, p & 15);
     }
     {
       const uint8_t* bp = nullptr;
@@ -478,7 +516,7 @@ __global__ void __launch_bounds__(kUpThreads, 1) prefill_umma_kernel(PrefillArgs
           any_int2 = true;
         }
       }
-      if (any_int2) f.vw = *reinterpret_cast<const uint4*>(bp + kVcOff + ((vbq * 4 + (vtq & 3)) << 4));
+      if (any_int2) fetch_v(f, bp);
     }
   };
   // (scale, min) of the fetched token: key scales for kkb 0, value scales for kkb 1
@@ -495,11 +533,17 @@ __global__ void __launch_bounds__(kUpThreads, 1) prefill_umma_kernel(PrefillArgs
     // keys: 8 chunks of 8 channels into row ktk of K-block kkb
     const uint32_t kdst = sK + (uint32_t)b * kUpKBytes + (uint32_t)kkb * 8192u;
     unsigned char* kg = gb + (kdst - base);
-    if (f.ksrc == 1) {
+    if (BITS == 4 && f.ksrc == 1) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)  // word i of the K-block: channels 8 i .. 8 i + 7
+        *reinterpret_cast<uint4*>(kg + um_swz((uint32_t)ktk, (uint32_t)i * 16u)) =
+            word4_to_half2x4((&f.kr[(i >> 2) * (BITS / 2 - 1)].x)[i & 3]);
+    } else if (f.ksrc == 1) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         uint32_t e[8];
-        const uint32_t w = i == 0 ? f.kr0.x : i == 1 ? f.kr0.y : i == 2 ? f.kr0.z : f.kr0.w;
+        const uint4& kr0 = f.kr[0];
+        const uint32_t w = i == 0 ? kr0.x : i == 1 ? kr0.y : i == 2 ? kr0.z : kr0.w;
         word_to_half2x8<false>(w, e);
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh)
@@ -537,7 +581,7 @@ __global__ void __launch_bounds__(kUpThreads, 1) prefill_umma_kernel(PrefillArgs
         float s_, m_;
         token_sm(f, k, s_, m_);
         if (f.ksrc == 1) {
-          ms.vsm[b][ktk * NG + k] = make_float2(0.5f * s_, fmaf(1.5f, s_, m_));  // centred codes
+          ms.vsm[b][ktk * NG + k] = make_float2(0.5f * s_, fmaf(BITS == 4 ? 7.5f : 1.5f, s_, m_));  // centred codes
           vmx = fmaxf(vmx, 0.5f * s_);
         } else {
           ms.vsm[b][ktk * NG + k] = make_float2(s_, m_);
@@ -551,8 +595,19 @@ __global__ void __launch_bounds__(kUpThreads, 1) prefill_umma_kernel(PrefillArgs
     // values: channels 16 vbq + ch, token pairs (2 vtq + s): one 32-bit word per
     // (channel, pair); pr[ch][s0] is the pair stored at position s0 ^ flip
     uint32_t pr[16][2];
-    if (f.vsrc[0] == 1 && f.vsrc[1] == 1 && f.vsrc[2] == 1 && f.vsrc[3] == 1) {
-      const uint32_t ws[4] = {f.vw.x, f.vw.y, f.vw.z, f.vw.w};  // word b': channels 4 b' .. + 3 of tokens 0..3
+    const bool quad = f.vsrc[0] == 1 && f.vsrc[1] == 1 && f.vsrc[2] == 1 && f.vsrc[3] == 1;
+    if (BITS == 4 && quad) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {  // word j: channels 16 j + 2 vbq (low halves), + 1 of tokens 0..3
+        const uint32_t w = (&f.vw[(j >> 2) * (BITS / 2 - 1)].x)[j & 3];
+        const uint32_t x01 = __byte_perm(w, 0u, sel_a), x23 = __byte_perm(w, 0u, sel_b);
+        pr[2 * j][0] = centred4_to_half2(x01 << 1);
+        pr[2 * j][1] = centred4_to_half2(x23 << 1);
+        pr[2 * j + 1][0] = centred4_to_half2(x01 >> 3);
+        pr[2 * j + 1][1] = centred4_to_half2(x23 >> 3);
+      }
+    } else if (quad) {
+      const uint32_t ws[4] = {f.vw[0].x, f.vw[0].y, f.vw[0].z, f.vw[0].w};  // word b': channels 4 b' .. + 3 of tokens 0..3
 #pragma unroll
       for (int bb = 0; bb < 4; ++bb) {
         const uint32_t x01 = __byte_perm(ws[bb], 0u, sel_a);  // the pair's two tokens in bytes 0, 2
@@ -570,10 +625,20 @@ __global__ void __launch_bounds__(kUpThreads, 1) prefill_umma_kernel(PrefillArgs
       uint32_t e[4][8];  // per token: fp16 pairs of adjacent channels
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        if (f.vsrc[i] == 1) {
+        if (BITS == 4 && f.vsrc[i] == 1) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {  // token i's byte of word j: the low half, then the high one
+            const uint32_t w = (&f.vw[(j >> 2) * (BITS / 2 - 1)].x)[j & 3] >> (8 * i);
+            e[i][j] = centred4_to_half2(((w & 0xFu) << 1) | ((w & 0xF0u) << 13));
+          }
+        } else if (f.vsrc[i] == 1) {
           const uint32_t sel = (uint32_t)(i | ((4 + i) << 4));
-          const uint32_t t01 = __byte_perm(f.vw.x, f.vw.y, sel), t23 = __byte_perm(f.vw.z, f.vw.w, sel);
+          const uint32_t t01 = __byte_perm(f.vw[0].x, f.vw[0].y, sel), t23 = __byte_perm(f.vw[0].z, f.vw[0].w, sel);
           word_to_half2x8<true>(__byte_perm(t01, t23, 0x5410u), e[i]);
+        } else if (BITS == 4 && f.vsrc[i] == 2) {
+          const __half* x = fp16_row(f.p0 + 4 * vtq + i, 1);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) e[i][j] = *reinterpret_cast<const uint32_t*>(x + vchan(j));
         } else if (f.vsrc[i] == 2) {
           const uint4* x = reinterpret_cast<const uint4*>(fp16_row(f.p0 + 4 * vtq + i, 1) + 16 * vbq);
           const uint4 x0 = x[0], x1 = x[1];
@@ -598,7 +663,7 @@ __global__ void __launch_bounds__(kUpThreads, 1) prefill_umma_kernel(PrefillArgs
     for (int ch = 0; ch < 16; ++ch)
 #pragma unroll
       for (int s0 = 0; s0 < 2; ++s0)
-        *reinterpret_cast<uint32_t*>(vg + um_swz((uint32_t)(16 * vbq + ch), (uint32_t)(2 * vtq + (s0 ^ flip)) * 4u)) =
+        *reinterpret_cast<uint32_t*>(vg + um_swz((uint32_t)(vchan(ch >> 1) + (ch & 1)), (uint32_t)(2 * vtq + (s0 ^ flip)) * 4u)) =
             pr[ch][s0];
   };
   if (warp >= kUpSmxWarps && warp < kUpMmaWarp) {
@@ -1058,11 +1123,20 @@ __global__ void __launch_bounds__(256) prefill_unrotate_kernel(PrefillArgs a) {
     for (int rr = 0; rr < 8; ++rr) {
       const int rk = r0 + rb + rr;
       if (rk < nrows) {
-        float* dst = a.out + (size_t)rt_row(a, hk, rk) * kD;
-        dst[lane] = acc[rr][0].x;
-        dst[lane + 32] = acc[rr][0].y;
-        dst[lane + 64] = acc[rr][1].x;
-        dst[lane + 96] = acc[rr][1].y;
+        const size_t at = (size_t)rt_row(a, hk, rk) * kD + lane;
+        if (a.out_bf16) {
+          __nv_bfloat16* dst = (__nv_bfloat16*)a.out + at;
+          dst[0] = __float2bfloat16_rn(acc[rr][0].x);
+          dst[32] = __float2bfloat16_rn(acc[rr][0].y);
+          dst[64] = __float2bfloat16_rn(acc[rr][1].x);
+          dst[96] = __float2bfloat16_rn(acc[rr][1].y);
+        } else {
+          float* dst = (float*)a.out + at;
+          dst[0] = acc[rr][0].x;
+          dst[32] = acc[rr][0].y;
+          dst[64] = acc[rr][1].x;
+          dst[96] = acc[rr][1].y;
+        }
       }
     }
   }
@@ -1081,7 +1155,7 @@ size_t prefill_workspace_bytes(int T, int hq) {
 }
 
 okv_status launch_prefill(const okv_cache_desc* d, const void* q, int T, int slot, int context_len,
-                          const int32_t* block_table, float* out, void* ws, cudaStream_t s) {
+                          const int32_t* block_table, void* out, void* ws, cudaStream_t s) {
   PrefillArgs a;
   a.q = (const __nv_bfloat16*)q;
   a.block_table = block_table;
@@ -1106,8 +1180,9 @@ okv_status launch_prefill(const okv_cache_desc* d, const void* q, int T, int slo
   a.hq = d->num_q_heads;
   a.hkv = d->num_kv_heads;
   a.g = a.hq / a.hkv;
-  a.ng = kD / d->group;
-  a.bhb = block_head_bytes(a.ng);
+  a.out_bf16 = out_bf16(d);
+  a.ng = kD / group_channels(d);
+  a.bhb = block_head_bytes(a.ng, code_bits(d));
   a.slot = slot;
   a.L = context_len;
   a.first = context_len - T;
@@ -1123,29 +1198,14 @@ okv_status launch_prefill(const okv_cache_desc* d, const void* q, int T, int slo
   okv_status st = check_launch("prefill query rotation");
   if (st != OKV_OK) return st;
   const dim3 grid((unsigned)((T * a.g + kPfRows - 1) / kPfRows), (unsigned)a.hkv);
-  switch (a.ng) {
-    case 1: {
-      static std::atomic<uint32_t> up_attr{0};
-      cudaError_t e1 = set_smem_limit_once((const void*)prefill_umma_kernel<1>, (int)kUpSmem, up_attr);
-      if (e1 != cudaSuccess) return fail(OKV_ERR_CUDA, "prefill attention smem attribute: %s", cudaGetErrorString(e1));
-      prefill_umma_kernel<1><<<grid, kUpThreads, kUpSmem, s>>>(a);
-      break;
-    }
-    case 2: {
-      static std::atomic<uint32_t> up2_attr{0};
-      cudaError_t e1 = set_smem_limit_once((const void*)prefill_umma_kernel<2>, (int)kUpSmem, up2_attr);
-      if (e1 != cudaSuccess) return fail(OKV_ERR_CUDA, "prefill attention smem attribute: %s", cudaGetErrorString(e1));
-      prefill_umma_kernel<2><<<grid, kUpThreads, kUpSmem, s>>>(a);
-      break;
-    }
-    default: {
-      static std::atomic<uint32_t> up4_attr{0};
-      cudaError_t e1 = set_smem_limit_once((const void*)prefill_umma_kernel<4>, (int)kUpSmem, up4_attr);
-      if (e1 != cudaSuccess) return fail(OKV_ERR_CUDA, "prefill attention smem attribute: %s", cudaGetErrorString(e1));
-      prefill_umma_kernel<4><<<grid, kUpThreads, kUpSmem, s>>>(a);
-      break;
-    }
-  }
+  using Kernel = void (*)(PrefillArgs);
+  static const Kernel kernels[2][3] = {{prefill_umma_kernel<1, 2>, prefill_umma_kernel<2, 2>, prefill_umma_kernel<4, 2>},
+                                       {prefill_umma_kernel<1, 4>, prefill_umma_kernel<2, 4>, prefill_umma_kernel<4, 4>}};
+  static std::atomic<uint32_t> up_attr[2][3];  // per instantiation: ng = 1, 2, 4 -> 0, 1, 2
+  const int fi = code_bits(d) == 4, gi = a.ng >> 1;
+  const cudaError_t e1 = set_smem_limit_once((const void*)kernels[fi][gi], (int)kUpSmem, up_attr[fi][gi]);
+  if (e1 != cudaSuccess) return fail(OKV_ERR_CUDA, "prefill attention smem attribute: %s", cudaGetErrorString(e1));
+  kernels[fi][gi]<<<grid, kUpThreads, kUpSmem, s>>>(a);
   st = check_launch("prefill attention");
   if (st != OKV_OK) return st;
   // The un-rotation may start (programmatic launch) while the attention's last

@@ -23,6 +23,7 @@ HEADER = os.path.join(os.path.dirname(_HERE), "include", "okv.h")
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_CUDA, ERR_NUMERIC, ERR_IO = range(6)
 DEV_BAD_BLOCK, DEV_BAD_POS, DEV_BAD_SLOT, DEV_TIMEOUT, DEV_NO_BLOCKS, DEV_NO_ROWS = 1, 2, 4, 8, 16, 32
 PRE_ROTATED = 1
+INT4, OUT_BF16, PAD_ROWS = 0x10000, 0x20000, 0x40000  # format bits of CacheDesc.group
 HEAD_DIM, BLOCK_TOKENS, WINDOW, BLOCK_HEAD_BYTES = 128, 16, 128, 1152
 
 
@@ -196,15 +197,22 @@ def calibrate_rotations(q: np.ndarray, k: np.ndarray, v: np.ndarray, hq: int, hk
 # ---------------------------------------------------------------------- cache
 
 class Cache:
-    """Device buffers of one layer's INT2 cache plus its C descriptor.
+    """Device buffers of one layer's quantised cache plus its C descriptor.
 
+    bits: 2 (INT2 codes, the default) or 4 (INT4).  pad_rows: appended rows
+    whose sequence slot is -1 are padding (else they raise DEV_BAD_SLOT).
     Memory comes from torch (the caller's allocator); the library only
     receives pointers."""
 
     def __init__(self, hq: int, hkv: int, num_blocks: int, num_seq_slots: int, max_blocks_per_seq: int,
-                 u_k, u_v, device="cuda", num_sink: int = 0, group: int = HEAD_DIM, stage_r: bool = True):
+                 u_k, u_v, device="cuda", num_sink: int = 0, group: int = HEAD_DIM, stage_r: bool = True,
+                 bits: int = 2, pad_rows: bool = False):
         import torch
-        self.hq, self.hkv, self.num_sink, self.group = hq, hkv, num_sink, group
+        if bits not in (2, 4):
+            raise ValueError(f"bits must be 2 or 4, got {bits}")
+        self.hq, self.hkv, self.num_sink, self.group, self.bits = hq, hkv, num_sink, group, bits
+        if bits == 4:
+            group |= INT4
         self.num_blocks, self.num_seq_slots, self.max_blocks_per_seq = num_blocks, num_seq_slots, max_blocks_per_seq
         self.block_head_bytes = int(lib().okv_block_head_bytes(group))
         nbytes = lib().okv_pages_bytes(num_blocks, hkv, group)
@@ -219,7 +227,7 @@ class Cache:
         # the prefill append's staged R of every (KV head, K|V), built once from U
         self.r_image = torch.empty(max(int(lib().okv_r_image_bytes(hkv)), 16), dtype=torch.uint8, device=device) \
             if stage_r else None
-        self.desc = CacheDesc(hq, hkv, HEAD_DIM, group, BLOCK_TOKENS, WINDOW, num_blocks, num_seq_slots,
+        self.desc = CacheDesc(hq, hkv, HEAD_DIM, group | (PAD_ROWS if pad_rows else 0), BLOCK_TOKENS, WINDOW, num_blocks, num_seq_slots,
                               max_blocks_per_seq, num_sink, self.pages.data_ptr(), self.ring.data_ptr(),
                               self.u_k.data_ptr(), self.u_v.data_ptr(), self.status.data_ptr(),
                               self.sink.data_ptr() if num_sink > 0 else None,
@@ -229,13 +237,26 @@ class Cache:
 
     def rebuild_r_image(self, stream=None):
         """Stage R from u_k, u_v into the image buffer again (after changing them)."""
-        _check(lib().okv_build_r_image(ctypes.byref(self.desc), _stream(stream)))
+        with _on(self.pages):
+            _check(lib().okv_build_r_image(ctypes.byref(self.desc), _stream(stream)))
 
     def device_status(self) -> int:
         return int(self.status[0].item())
 
     def clear_status(self):
         self.status.zero_()
+
+
+def _desc_for(cache: Cache, out):
+    """The cache's descriptor for a call that writes `out`: fp32, or bf16 (the OUT_BF16 format bit)."""
+    import torch
+    if out.dtype != torch.bfloat16:
+        _need(out, torch.float32, "out")
+        return cache.desc
+    _need(out, torch.bfloat16, "out")
+    d = CacheDesc.from_buffer_copy(cache.desc)
+    d.group |= OUT_BF16
+    return d
 
 
 def save_rotations(path, u_k, u_v, tag: str = "") -> None:
@@ -276,9 +297,10 @@ def append_quantize(cache: Cache, k, v, seq_slot, pos, block_table, slot_lens, p
     if rotated_out is not None:
         _need(rotated_out, torch.float32, "rotated_out")
     T = k.shape[0] if k.dim() > 0 else 0
-    _check(lib().okv_append_quantize(ctypes.byref(cache.desc), _ptr(k), _ptr(v), T, _ptr(seq_slot), _ptr(pos),
-                                     _ptr(block_table), _ptr(slot_lens), PRE_ROTATED if pre_rotated else 0,
-                                     _ptr(rotated_out), _stream(stream)))
+    with _on(k):
+        _check(lib().okv_append_quantize(ctypes.byref(cache.desc), _ptr(k), _ptr(v), T, _ptr(seq_slot), _ptr(pos),
+                                         _ptr(block_table), _ptr(slot_lens), PRE_ROTATED if pre_rotated else 0,
+                                         _ptr(rotated_out), _stream(stream)))
 
 
 def decode_workspace_bytes(cache: Cache, batch: int) -> int:
@@ -298,11 +320,12 @@ def decode_attention(cache: Cache, q, seq_slot, block_table, context_lens, out=N
     batch = q.shape[0]
     if out is None:
         out = torch.empty((batch, cache.hq, HEAD_DIM), dtype=torch.float32, device=q.device)
-    _need(out, torch.float32, "out")
+    desc = _desc_for(cache, out)
     if ws is None:
         ws = workspace(cache, batch)
-    _check(lib().okv_decode_attention(ctypes.byref(cache.desc), _ptr(q), batch, _ptr(seq_slot), _ptr(block_table),
-                                      _ptr(context_lens), _ptr(out), _ptr(ws), ws.numel(), _stream(stream)))
+    with _on(q):
+        _check(lib().okv_decode_attention(ctypes.byref(desc), _ptr(q), batch, _ptr(seq_slot), _ptr(block_table),
+                                          _ptr(context_lens), _ptr(out), _ptr(ws), ws.numel(), _stream(stream)))
     return out
 
 
@@ -318,12 +341,13 @@ def decode_step(cache: Cache, k, v, new_seq_slot, new_pos, slot_lens, q, seq_slo
     T = k.shape[0]
     if out is None:
         out = torch.empty((B, cache.hq, HEAD_DIM), dtype=torch.float32, device=q.device)
-    _need(out, torch.float32, "out")
+    desc = _desc_for(cache, out)
     if ws is None:
         ws = workspace(cache, B)
-    _check(lib().okv_decode_step(ctypes.byref(cache.desc), _ptr(k), _ptr(v), T, _ptr(new_seq_slot), _ptr(new_pos),
-                                 _ptr(slot_lens), _ptr(q), B, _ptr(seq_slot), _ptr(block_table), _ptr(context_lens),
-                                 _ptr(out), _ptr(ws), ws.numel(), _stream(stream)))
+    with _on(q):
+        _check(lib().okv_decode_step(ctypes.byref(desc), _ptr(k), _ptr(v), T, _ptr(new_seq_slot), _ptr(new_pos),
+                                     _ptr(slot_lens), _ptr(q), B, _ptr(seq_slot), _ptr(block_table),
+                                     _ptr(context_lens), _ptr(out), _ptr(ws), ws.numel(), _stream(stream)))
     return out
 
 
@@ -346,14 +370,14 @@ class DecodeStepCall:
         B = q.shape[0]
         if out is None:
             out = torch.empty((B, cache.hq, HEAD_DIM), dtype=torch.float32, device=q.device)
-        _need(out, torch.float32, "out")
+        desc = _desc_for(cache, out)
         if ws is None:
             ws = workspace(cache, B)
-        self.out, self._keep = out, (cache, k, v, new_seq_slot, new_pos, slot_lens, q, seq_slot, block_table,
+        self.out, self._keep = out, (cache, desc, k, v, new_seq_slot, new_pos, slot_lens, q, seq_slot, block_table,
                                       context_lens, ws)
         self._fn = lib().okv_decode_step
         self._stream = stream
-        self._args = (ctypes.byref(cache.desc), _ptr(k), _ptr(v), k.shape[0], _ptr(new_seq_slot), _ptr(new_pos),
+        self._args = (ctypes.byref(desc), _ptr(k), _ptr(v), k.shape[0], _ptr(new_seq_slot), _ptr(new_pos),
                       _ptr(slot_lens), _ptr(q), B, _ptr(seq_slot), _ptr(block_table), _ptr(context_lens), _ptr(out),
                       _ptr(ws), ws.numel())
         self._want_graph, self._graph = graph, None
@@ -391,9 +415,10 @@ def decode_attention_noalloc(cache: Cache, q, seq_slot, block_table, context_len
     batch = q.shape[0]
     if out is None:
         out = torch.empty((batch, cache.hq, HEAD_DIM), dtype=torch.float32, device=q.device)
-    _need(out, torch.float32, "out")
-    _check(lib().okv_decode_attention_noalloc(ctypes.byref(cache.desc), _ptr(q), batch, _ptr(seq_slot),
-                                              _ptr(block_table), _ptr(context_lens), _ptr(out), _stream(stream)))
+    desc = _desc_for(cache, out)
+    with _on(q):
+        _check(lib().okv_decode_attention_noalloc(ctypes.byref(desc), _ptr(q), batch, _ptr(seq_slot),
+                                                  _ptr(block_table), _ptr(context_lens), _ptr(out), _stream(stream)))
     return out
 
 
@@ -410,11 +435,12 @@ def prefill_attention(cache: Cache, q, slot: int, context_len: int, block_table,
     T = q.shape[0]
     if out is None:
         out = torch.empty((T, cache.hq, HEAD_DIM), dtype=torch.float32, device=q.device)
-    _need(out, torch.float32, "out")
+    desc = _desc_for(cache, out)
     if ws is None:
         ws = torch.empty(max(prefill_workspace_bytes(cache, T), 256), dtype=torch.uint8, device=q.device)
-    _check(lib().okv_prefill_attention(ctypes.byref(cache.desc), _ptr(q), T, int(slot), int(context_len),
-                                       _ptr(block_table), _ptr(out), _ptr(ws), ws.numel(), _stream(stream)))
+    with _on(q):
+        _check(lib().okv_prefill_attention(ctypes.byref(desc), _ptr(q), T, int(slot), int(context_len),
+                                           _ptr(block_table), _ptr(out), _ptr(ws), ws.numel(), _stream(stream)))
     return out
 
 
@@ -553,7 +579,8 @@ def dequantize(cache: Cache, seq_slot, block_table, context_lens, max_ctx: int, 
     batch = seq_slot.shape[0]
     if out is None:
         out = torch.empty((batch, cache.hkv, max_ctx, HEAD_DIM), dtype=torch.float32, device="cuda")
-    _need(out, torch.float32, "out")
-    _check(lib().okv_dequantize(ctypes.byref(cache.desc), batch, _ptr(seq_slot), _ptr(block_table),
-                                _ptr(context_lens), max_ctx, which, basis, source, _ptr(out), _stream(stream)))
+    desc = _desc_for(cache, out)
+    with _on(out):
+        _check(lib().okv_dequantize(ctypes.byref(desc), batch, _ptr(seq_slot), _ptr(block_table),
+                                    _ptr(context_lens), max_ctx, which, basis, source, _ptr(out), _stream(stream)))
     return out

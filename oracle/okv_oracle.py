@@ -210,8 +210,9 @@ def fp16_saturate(x32: np.ndarray) -> np.ndarray:
     return x.astype(np.float16)
 
 
-def quantize(z32: np.ndarray, group: int = D):
+def quantize(z32: np.ndarray, group: int = D, bits: int = 2):
     """Quantise groups of fp32 values to 2-bit codes with fp16 scale and min.
+    (bits = 4: sixteen levels, 15 and 0..15 in the place of 3 and 0..3.)
 
     z32: float32 [..., 128].  With group = 128 (the built format: one group
     per row) returns (codes uint8 [..., 128], s16 float16 [...], m16 float16
@@ -231,24 +232,24 @@ def quantize(z32: np.ndarray, group: int = D):
     if group <= 0 or D % group != 0:
         raise ValueError("group must divide 128")
     if group != D:
-        c, s16, m16 = quantize_rows(z.reshape(*z.shape[:-1], D // group, group))
+        c, s16, m16 = quantize_rows(z.reshape(*z.shape[:-1], D // group, group), bits)
         return c.reshape(z.shape), s16, m16
-    return quantize_rows(z)
+    return quantize_rows(z, bits)
 
 
-def quantize_rows(z: np.ndarray):
+def quantize_rows(z: np.ndarray, bits: int = 2):
     """The rule of `quantize` applied to each row (last axis) of fp32 z."""
     z = np.asarray(z, dtype=np.float32)
     mn = z.min(axis=-1)
     mx = z.max(axis=-1)
-    s32 = (mx - mn) / np.float32(3.0)
+    s32 = (mx - mn) / np.float32(2 ** bits - 1)
     s16 = fp16_saturate(s32)
     m16 = fp16_saturate(mn)
     s = s16.astype(np.float32)[..., None]
     m = m16.astype(np.float32)[..., None]
     with np.errstate(divide="ignore", invalid="ignore"):
         t = (z - m) / np.where(s == 0, np.float32(1.0), s)
-    c = np.clip(np.rint(t), 0, 3)
+    c = np.clip(np.rint(t), 0, 2 ** bits - 1)
     c = np.where(s == 0, 0, c).astype(np.uint8)
     return c, s16, m16
 
@@ -291,8 +292,9 @@ class Cache:
     """
 
     def __init__(self, hkv: int, u_k: np.ndarray, u_v: np.ndarray, window: int = W, sinks: int = 0,
-                 group: int = D):
+                 group: int = D, bits: int = 2):
         self.hkv = hkv
+        self.bits = bits    # bits per code
         self.window = window
         self.sinks = sinks
         self.group = group  # channels per quantisation group (128: one per token-head)
@@ -331,7 +333,7 @@ class Cache:
             for h in range(self.hkv):
                 xs = np.asarray(x[:, h, :], dtype=np.float32)
                 z = xs if pre_rotated else (xs.astype(np.float64) @ self.r[kind][h]).astype(np.float32)
-                c, s16, m16 = quantize(z, self.group)
+                c, s16, m16 = quantize(z, self.group, self.bits)
                 st = self._store(slot, kind, h, pos0 + n)
                 sl = slice(pos0, pos0 + n)
                 st["codes"][sl], st["s16"][sl], st["m16"][sl] = c, s16, m16

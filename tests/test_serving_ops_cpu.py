@@ -104,3 +104,48 @@ def test_binding_checks_types_and_shapes_on_the_host():
         p.build(i.long(), i, i, i, i, i, i)
     with pytest.raises(ValueError, match="CUDA"):
         p.build(i, i, i, i.view(1, 2), i, i, i)
+
+
+def _desc(group=128, **kw):
+    d = okv.CacheDesc(32, 8, 128, group, 16, 128, 64, 4, 16, 0, 4096, 8192, 16384, 32768, 0)
+    for k, v in kw.items():
+        setattr(d, k, v)
+    return d
+
+
+def test_format_bits_of_the_group():
+    lib = okv.lib()
+    for bits in (0, okv.OUT_BF16, okv.PAD_ROWS, okv.OUT_BF16 | okv.PAD_ROWS):
+        assert [lib.okv_block_head_bytes(g | bits) for g in (128, 64, 32, 16, 0)] == [1152, 1280, 1536, 0, 0]
+        assert [lib.okv_block_head_bytes(g | bits | okv.INT4) for g in (128, 64, 32, 16, 0)] == [2176, 2304, 2560, 0, 0]
+    assert lib.okv_pages_bytes(10, 8, 64 | okv.INT4) == 10 * 8 * 2304
+    for group in (okv.INT4, 16 | okv.INT4, 128 | 0x80000, 256 | okv.OUT_BF16, -128):
+        d = _desc(group)
+        assert lib.okv_append_quantize(ctypes.byref(d), FAKE, FAKE, 1, FAKE, FAKE, FAKE, FAKE, 0, None, None) \
+            == okv.ERR_UNSUPPORTED, group
+    for group in (128 | okv.INT4, 32 | okv.INT4 | okv.OUT_BF16 | okv.PAD_ROWS):
+        d = _desc(group)
+        assert lib.okv_append_quantize(ctypes.byref(d), None, None, 0, None, None, None, None, 0, None, None) == okv.OK
+        assert lib.okv_decode_workspace_bytes(ctypes.byref(d), 4) > 0
+
+
+def test_attention_refuses_misaligned_tensors():
+    lib = okv.lib()
+    ws = 1 << 24
+    for group, odd in ((128, 2), (128 | okv.OUT_BF16, 1), (128 | okv.INT4, 2)):
+        d = _desc(group)
+        assert lib.okv_decode_attention(ctypes.byref(d), FAKE, 4, FAKE, FAKE, FAKE, FAKE + odd, ws, 1 << 30, None) \
+            == okv.ERR_INVALID_ARG
+        assert lib.okv_decode_attention_noalloc(ctypes.byref(d), FAKE, 4, FAKE, FAKE, FAKE, FAKE + odd, None) \
+            == okv.ERR_INVALID_ARG
+        assert lib.okv_prefill_attention(ctypes.byref(d), FAKE, 4, 0, 64, FAKE, FAKE + odd, ws, 1 << 30, None) \
+            == okv.ERR_INVALID_ARG
+        # the prefill's query rotation reads 16 bytes at a time
+        for off in (2, 8):
+            assert lib.okv_prefill_attention(ctypes.byref(d), FAKE + off, 4, 0, 64, FAKE, FAKE, ws, 1 << 30, None) \
+                == okv.ERR_INVALID_ARG
+
+
+def test_cache_takes_two_or_four_bits():
+    with pytest.raises(ValueError, match="bits"):
+        okv.Cache(4, 1, 4, 1, 4, None, None, bits=3)
