@@ -152,9 +152,11 @@ __global__ void __launch_bounds__(kPlThreads) plan_scan_kernel(PlanArgs a) {
                                (st > (uint32_t)p.max_tokens ? OKV_DEV_NO_ROWS : 0u);
     // The sums grow with b, so the requests served are a prefix of the live
     // ones, and a served request's sums hold served requests only.
-    if (took) {
-      atomicMax(&s_used[0], sb);
-      atomicMax(&s_used[1], st);
+    const uint32_t top_b = __reduce_max_sync(0xffffffffu, took ? sb : 0u);
+    const uint32_t top_t = __reduce_max_sync(0xffffffffu, took ? st : 0u);
+    if ((tid & 31) == 0) {
+      atomicMax(&s_used[0], top_b);
+      atomicMax(&s_used[1], top_t);
     }
     __syncthreads();
     used_b = s_used[0];
@@ -181,7 +183,8 @@ __global__ void __launch_bounds__(kPlThreads) plan_scan_kernel(PlanArgs a) {
     base_b = sat_add(base_b, total.x);
     base_t = sat_add(base_t, total.y);
   }
-  if (flags != 0u) raise_flag(p.status_word, flags);
+  flags = __reduce_or_sync(0xffffffffu, flags);  // (one atomic per warp: 300 of one word took 10 us)
+  if (flags != 0u && (tid & 31) == 0) raise_flag(p.status_word, flags);
   const int total_rows = (int)used_t;
   if (tid == 0) {
     p.cu_tokens[B] = total_rows;
@@ -222,7 +225,9 @@ __global__ void __launch_bounds__(kPlFillThreads) plan_fill_kernel(PlanArgs a) {
   for (int i = 0; i < kPlRows; ++i) {
     const int row = (int)r0 + i;
     // rows of one thread nearly always share a request: step on from the last one's
-    while (lo + 1 < B && p.cu_tokens[lo + 1] <= row) ++lo;
+    // (not past the last token: the requests behind it all start there)
+    if (row < total)
+      while (lo + 1 < B && p.cu_tokens[lo + 1] <= row) ++lo;
     plan_row(p, row, lo, lo, total, count, [&](int b) { return p.cu_tokens[b]; }, [&](int b) { return p.seq_slot[b]; },
              [&](int b) { return a.old_len[b]; }, [&](int b) { return a.blk_off[b]; }, slot[i], pos[i]);
   }

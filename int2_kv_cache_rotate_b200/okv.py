@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes
 import os
 import re
+import struct
 
 import numpy as np
 
@@ -74,6 +75,10 @@ class NormRopeArgs(ctypes.Structure):
                                                "v_out")]
 
 
+# the same two structures as bytes, for calls that fill every field at once
+_PLAN, _ROPE = struct.Struct("5i4x13P"), struct.Struct("8i2f3P6q7P")
+assert _PLAN.size == ctypes.sizeof(PlanArgs) and _ROPE.size == ctypes.sizeof(NormRopeArgs)
+
 _lib = None
 _P = ctypes.c_void_p
 _I32 = ctypes.c_int32
@@ -103,8 +108,8 @@ _SIGNATURES = {
     "okv_prefill_attention": (_I32, [_DESC, _P, _I32, _I32, _I32, _P, _P, _P, _SZ, _P]),
     "okv_decode_step": (_I32, [_DESC, _P, _P, _I32, _P, _P, _P, _P, _I32, _P, _P, _P, _P, _P, _SZ, _P]),
     "okv_plan_workspace_bytes": (_SZ, [_I32]),
-    "okv_plan_append": (_I32, [ctypes.POINTER(PlanArgs), _P, _SZ, _P]),
-    "okv_qk_norm_rope": (_I32, [ctypes.POINTER(NormRopeArgs), _P]),
+    "okv_plan_append": (_I32, [_P, _P, _SZ, _P]),
+    "okv_qk_norm_rope": (_I32, [_P, _P]),
     "okv_save_rotations": (_I32, [ctypes.c_char_p, _I32, _I32, _I32, _P, _P, ctypes.c_char_p]),
     "okv_rotations_file_shape": (_I32, [ctypes.c_char_p, _P, _P, _P, _P]),
     "okv_load_rotations": (_I32, [ctypes.c_char_p, _I32, _I32, _I32, _P, _P, _P, _SZ, _I32]),
@@ -143,35 +148,40 @@ def _ptr(t) -> int:
     return 0 if t is None else t.data_ptr()
 
 
+_torch = None
+
+
+def _t():
+    """torch, imported on first use (the host-only calls do not need it)."""
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch
+
+
 def _stream(stream) -> int:
-    import torch
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    return stream.cuda_stream
+    return (_t().cuda.current_stream() if stream is None else stream).cuda_stream
 
 
-class _Same:
-    def __enter__(self):
-        pass
-
-    def __exit__(self, *exc):
-        pass
-
-
-_SAME = _Same()
-
-
-def _on(t):
-    """The device of tensor t as the current one (a launch and the current stream belong to the current device)."""
-    import torch
-    return _SAME if t.device.index == torch.cuda.current_device() else torch.cuda.device(t.device)
+def _run(t, stream, fn, *args):
+    """fn(*args, stream handle) with the device of tensor t as the current one: a launch, and the default current
+    stream, belong to the current device."""
+    torch = _t()
+    dev = t.get_device()
+    if dev == torch._C._cuda_getDevice():
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, _stream(stream))
+    if status != OK:
+        _check(status)
 
 
 def _need(t, dtype, name, device=True):
-    import torch
     if t is None:
         raise ValueError(f"{name} is required")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if device and not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
@@ -237,8 +247,7 @@ class Cache:
 
     def rebuild_r_image(self, stream=None):
         """Stage R from u_k, u_v into the image buffer again (after changing them)."""
-        with _on(self.pages):
-            _check(lib().okv_build_r_image(ctypes.byref(self.desc), _stream(stream)))
+        _run(self.pages, stream, lib().okv_build_r_image, ctypes.byref(self.desc))
 
     def device_status(self) -> int:
         return int(self.status[0].item())
@@ -249,8 +258,8 @@ class Cache:
 
 def _desc_for(cache: Cache, out):
     """The cache's descriptor for a call that writes `out`: fp32, or bf16 (the OUT_BF16 format bit)."""
-    import torch
-    if out.dtype != torch.bfloat16:
+    torch = _t()
+    if out.dtype is not torch.bfloat16:
         _need(out, torch.float32, "out")
         return cache.desc
     _need(out, torch.bfloat16, "out")
@@ -297,10 +306,8 @@ def append_quantize(cache: Cache, k, v, seq_slot, pos, block_table, slot_lens, p
     if rotated_out is not None:
         _need(rotated_out, torch.float32, "rotated_out")
     T = k.shape[0] if k.dim() > 0 else 0
-    with _on(k):
-        _check(lib().okv_append_quantize(ctypes.byref(cache.desc), _ptr(k), _ptr(v), T, _ptr(seq_slot), _ptr(pos),
-                                         _ptr(block_table), _ptr(slot_lens), PRE_ROTATED if pre_rotated else 0,
-                                         _ptr(rotated_out), _stream(stream)))
+    _run(k, stream, lib().okv_append_quantize, ctypes.byref(cache.desc), _ptr(k), _ptr(v), T, _ptr(seq_slot),
+         _ptr(pos), _ptr(block_table), _ptr(slot_lens), PRE_ROTATED if pre_rotated else 0, _ptr(rotated_out))
 
 
 def decode_workspace_bytes(cache: Cache, batch: int) -> int:
@@ -313,7 +320,7 @@ def workspace(cache: Cache, batch: int):
 
 
 def decode_attention(cache: Cache, q, seq_slot, block_table, context_lens, out=None, ws=None, stream=None):
-    import torch
+    torch = _t()
     _need(q, torch.bfloat16, "q")
     for name, t in (("seq_slot", seq_slot), ("block_table", block_table), ("context_lens", context_lens)):
         _need(t, torch.int32, name)
@@ -323,16 +330,15 @@ def decode_attention(cache: Cache, q, seq_slot, block_table, context_lens, out=N
     desc = _desc_for(cache, out)
     if ws is None:
         ws = workspace(cache, batch)
-    with _on(q):
-        _check(lib().okv_decode_attention(ctypes.byref(desc), _ptr(q), batch, _ptr(seq_slot), _ptr(block_table),
-                                          _ptr(context_lens), _ptr(out), _ptr(ws), ws.numel(), _stream(stream)))
+    _run(q, stream, lib().okv_decode_attention, ctypes.byref(desc), _ptr(q), batch, _ptr(seq_slot),
+         _ptr(block_table), _ptr(context_lens), _ptr(out), _ptr(ws), ws.numel())
     return out
 
 
 def decode_step(cache: Cache, k, v, new_seq_slot, new_pos, slot_lens, q, seq_slot, block_table, context_lens,
                 out=None, ws=None, stream=None):
     """Append this step's bf16 tokens, then decode (one call; see okv_decode_step)."""
-    import torch
+    torch = _t()
     _need(k, torch.bfloat16, "k"), _need(v, torch.bfloat16, "v"), _need(q, torch.bfloat16, "q")
     for name, t in (("new_seq_slot", new_seq_slot), ("new_pos", new_pos), ("slot_lens", slot_lens),
                     ("seq_slot", seq_slot), ("block_table", block_table), ("context_lens", context_lens)):
@@ -344,10 +350,9 @@ def decode_step(cache: Cache, k, v, new_seq_slot, new_pos, slot_lens, q, seq_slo
     desc = _desc_for(cache, out)
     if ws is None:
         ws = workspace(cache, B)
-    with _on(q):
-        _check(lib().okv_decode_step(ctypes.byref(desc), _ptr(k), _ptr(v), T, _ptr(new_seq_slot), _ptr(new_pos),
-                                     _ptr(slot_lens), _ptr(q), B, _ptr(seq_slot), _ptr(block_table),
-                                     _ptr(context_lens), _ptr(out), _ptr(ws), ws.numel(), _stream(stream)))
+    _run(q, stream, lib().okv_decode_step, ctypes.byref(desc), _ptr(k), _ptr(v), T, _ptr(new_seq_slot),
+         _ptr(new_pos), _ptr(slot_lens), _ptr(q), B, _ptr(seq_slot), _ptr(block_table), _ptr(context_lens), _ptr(out),
+         _ptr(ws), ws.numel())
     return out
 
 
@@ -408,7 +413,7 @@ class DecodeStepCall:
 
 def decode_attention_noalloc(cache: Cache, q, seq_slot, block_table, context_lens, out=None, stream=None):
     """Decode attention with the library's static scratch (no workspace, no allocation in the library)."""
-    import torch
+    torch = _t()
     _need(q, torch.bfloat16, "q")
     for name, t in (("seq_slot", seq_slot), ("block_table", block_table), ("context_lens", context_lens)):
         _need(t, torch.int32, name)
@@ -416,9 +421,8 @@ def decode_attention_noalloc(cache: Cache, q, seq_slot, block_table, context_len
     if out is None:
         out = torch.empty((batch, cache.hq, HEAD_DIM), dtype=torch.float32, device=q.device)
     desc = _desc_for(cache, out)
-    with _on(q):
-        _check(lib().okv_decode_attention_noalloc(ctypes.byref(desc), _ptr(q), batch, _ptr(seq_slot),
-                                                  _ptr(block_table), _ptr(context_lens), _ptr(out), _stream(stream)))
+    _run(q, stream, lib().okv_decode_attention_noalloc, ctypes.byref(desc), _ptr(q), batch, _ptr(seq_slot),
+         _ptr(block_table), _ptr(context_lens), _ptr(out))
     return out
 
 
@@ -429,7 +433,7 @@ def prefill_workspace_bytes(cache: Cache, T: int) -> int:
 def prefill_attention(cache: Cache, q, slot: int, context_len: int, block_table, out=None, ws=None, stream=None):
     """Causal attention of a prefill chunk (q: bf16 [T, Hq, 128], already appended at positions
     context_len - T .. context_len - 1 of sequence `slot`) over the cache; returns fp32 [T, Hq, 128]."""
-    import torch
+    torch = _t()
     _need(q, torch.bfloat16, "q")
     _need(block_table, torch.int32, "block_table")
     T = q.shape[0]
@@ -438,9 +442,8 @@ def prefill_attention(cache: Cache, q, slot: int, context_len: int, block_table,
     desc = _desc_for(cache, out)
     if ws is None:
         ws = torch.empty(max(prefill_workspace_bytes(cache, T), 256), dtype=torch.uint8, device=q.device)
-    with _on(q):
-        _check(lib().okv_prefill_attention(ctypes.byref(desc), _ptr(q), T, int(slot), int(context_len),
-                                           _ptr(block_table), _ptr(out), _ptr(ws), ws.numel(), _stream(stream)))
+    _run(q, stream, lib().okv_prefill_attention, ctypes.byref(desc), _ptr(q), T, int(slot), int(context_len),
+         _ptr(block_table), _ptr(out), _ptr(ws), ws.numel())
     return out
 
 
@@ -470,39 +473,35 @@ class AppendPlan:
         self.free_count = torch.zeros(1, **i32)
         self.status = torch.zeros(4, **i32)
         self.ws = torch.empty(int(lib().okv_plan_workspace_bytes(batch)), dtype=torch.uint8, device=device)
-        self._fn = lib().okv_plan_append
-        self._args = PlanArgs(num_requests=batch, max_tokens=max_tokens, context_lens=self.context_lens.data_ptr(),
-                              cu_tokens=self.cu_tokens.data_ptr(), tok_slot=self.tok_slot.data_ptr(),
-                              tok_pos=self.tok_pos.data_ptr(), free_count_out=self.free_count.data_ptr(),
-                              status_word=self.status.data_ptr())
+        self._fn, self._dev = lib().okv_plan_append, self.tok_slot.get_device()
+        self._outs = tuple(t.data_ptr() for t in (self.context_lens, self.cu_tokens, self.tok_slot, self.tok_pos,
+                                                  self.free_count, self.status))
+        self._ws = (self.ws.data_ptr(), self.ws.numel())
 
     def build(self, seq_slot, cached_lens, new_lens, block_table, slot_lens, free_blocks, free_count, stream=None):
         """Plan one step: request b (sequence slot seq_slot[b], -1 for padding) holds cached_lens[b] tokens and
         gains new_lens[b].  Updates block_table [slots][columns] and slot_lens [slots]; takes blocks from the end
         of free_blocks[:free_count].  cached_lens may be this plan's context_lens and free_count its free_count
         (a step that feeds the next).  Returns self."""
-        import torch
+        i32, dev = _t().int32, self._dev
         for name, t in (("seq_slot", seq_slot), ("cached_lens", cached_lens), ("new_lens", new_lens),
                         ("block_table", block_table), ("slot_lens", slot_lens), ("free_blocks", free_blocks),
                         ("free_count", free_count)):
-            _need(t, torch.int32, name)
-            if t.device != self.tok_slot.device:
+            if t.dtype is not i32 or not t.is_contiguous() or t.get_device() != dev or dev < 0:
+                _need(t, i32, name)
                 raise ValueError(f"{name} must be on {self.tok_slot.device}")
+        n = self.batch
         for name, t in (("seq_slot", seq_slot), ("cached_lens", cached_lens), ("new_lens", new_lens)):
-            if t.shape != (self.batch,):
-                raise ValueError(f"{name} must have shape ({self.batch},), got {tuple(t.shape)}")
-        if block_table.dim() != 2 or slot_lens.shape != block_table.shape[:1]:
+            if t.dim() != 1 or t.shape[0] != n:
+                raise ValueError(f"{name} must have shape ({n},), got {tuple(t.shape)}")
+        if block_table.dim() != 2 or slot_lens.dim() != 1 or slot_lens.shape[0] != block_table.shape[0]:
             raise ValueError("block_table must be [slots][columns] and slot_lens [slots]")
         if free_blocks.dim() != 1 or free_count.numel() != 1:
             raise ValueError("free_blocks must be one-dimensional and free_count hold one value")
-        a = self._args
-        a.num_seq_slots, a.max_blocks_per_seq = block_table.shape
-        a.num_free = free_blocks.shape[0]
-        a.seq_slot, a.cached_lens, a.new_lens = seq_slot.data_ptr(), cached_lens.data_ptr(), new_lens.data_ptr()
-        a.block_table, a.slot_lens = block_table.data_ptr(), slot_lens.data_ptr()
-        a.free_blocks, a.free_count = free_blocks.data_ptr(), free_count.data_ptr()
-        with _on(self.tok_slot):
-            _check(self._fn(a, self.ws.data_ptr(), self.ws.numel(), _stream(stream)))
+        a = _PLAN.pack(n, self.max_tokens, *block_table.shape, free_blocks.shape[0], seq_slot.data_ptr(),
+                       cached_lens.data_ptr(), new_lens.data_ptr(), free_blocks.data_ptr(), free_count.data_ptr(),
+                       block_table.data_ptr(), slot_lens.data_ptr(), *self._outs)
+        _run(self.tok_slot, stream, self._fn, a, *self._ws)
         return self
 
     def device_status(self) -> int:
@@ -519,47 +518,52 @@ def qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps: f
     v [T][Hkv][128] in bf16, fp16 or fp32, views of one fused projection included (the last dimension contiguous,
     rows on 16-byte boundaries); positions int32 [T] (negative: a padding row, left as it is); inv_freq fp32
     [rot_dim/2]; weights fp32 [128].  Returns contiguous bf16 (q, k), or (q, k, v) when v is given."""
-    import torch
-    kinds = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
-    if q.dtype not in kinds:
+    torch = _t()
+    kind = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}.get(q.dtype)
+    if kind is None:
         raise TypeError(f"q must be bfloat16, float16 or float32, got {q.dtype}")
-    given = [("q", q), ("k", k)] + ([("v", v)] if v is not None else [])
-    for name, t in given:
-        if t.dtype != q.dtype:
+    given = (("q", q, q_out), ("k", k, k_out)) if v is None else (("q", q, q_out), ("k", k, k_out), ("v", v, v_out))
+    for name, t, _ in given:
+        if t.dtype is not q.dtype:
             raise TypeError(f"{name} must be {q.dtype} like q, got {t.dtype}")
-    for name, t in given:
-        if not t.is_cuda or t.device != q.device:
+    dev = q.get_device()
+    strides, ptrs, outs = [], [], []
+    for name, t, out in given:
+        if dev < 0 or t.get_device() != dev:
             raise ValueError(f"{name} must be a CUDA tensor on one device with q")
-        if t.dim() != 3 or t.shape[0] != q.shape[0] or t.shape[2] != HEAD_DIM or (t.shape[2] and t.stride(2) != 1):
-            raise ValueError(f"{name} must be [T][heads][{HEAD_DIM}] with contiguous rows, got {tuple(t.shape)}")
-    if v is not None and v.shape[1] != k.shape[1]:
-        raise ValueError("k and v must have the same number of heads")
-    _need(positions, torch.int32, "positions"), _need(inv_freq, torch.float32, "inv_freq")
-    if positions.shape != q.shape[:1]:
-        raise ValueError(f"positions must have shape ({q.shape[0]},)")
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is not None:
-            _need(w, torch.float32, name)
-            if w.shape != (HEAD_DIM,):
-                raise ValueError(f"{name} must have shape ({HEAD_DIM},)")
-    for name, t in (("positions", positions), ("inv_freq", inv_freq), ("q_weight", q_weight), ("k_weight", k_weight)):
-        if t is not None and t.device != q.device:
-            raise ValueError(f"{name} must be on {q.device}")
-    outs = []
-    for (name, t), out in zip(given, (q_out, k_out, v_out)):
+        shape, st = t.shape, t.stride()
+        if len(shape) != 3 or shape[0] != q.shape[0] or shape[2] != HEAD_DIM or st[2] != 1:
+            raise ValueError(f"{name} must be [T][heads][{HEAD_DIM}] with contiguous rows, got {tuple(shape)}")
+        strides += st[:2]
+        ptrs.append(t.data_ptr())
         if out is None:
-            out = torch.empty(t.shape, dtype=torch.bfloat16, device=t.device)
-        _need(out, torch.bfloat16, name + "_out")
-        if out.shape != t.shape or out.device != q.device:
-            raise ValueError(f"{name}_out must have shape {tuple(t.shape)} on {q.device}")
+            out = torch.empty(shape, dtype=torch.bfloat16, device=t.device)
+        elif out.dtype is not torch.bfloat16 or out.shape != shape or out.get_device() != dev or \
+                not out.is_contiguous():
+            _need(out, torch.bfloat16, name + "_out")
+            raise ValueError(f"{name}_out must have shape {tuple(shape)} on {q.device}")
         outs.append(out)
-    st = [x for _, t in given for x in (t.stride(0), t.stride(1))] + ([0, 0] if v is None else [])
-    a = NormRopeArgs(q.shape[0], q.shape[1], k.shape[1], HEAD_DIM, kinds[q.dtype], 2 * inv_freq.numel(),
-                     int(interleaved), int(norm), eps, rope_scale, _ptr(q), _ptr(k), _ptr(v), *st, _ptr(positions),
-                     _ptr(inv_freq), _ptr(q_weight), _ptr(k_weight), _ptr(outs[0]), _ptr(outs[1]),
-                     _ptr(outs[2]) if v is not None else 0)
-    with _on(q):
-        _check(lib().okv_qk_norm_rope(a, _stream(stream)))
+    tokens, hq, _ = q.shape
+    hkv = k.shape[1]
+    if v is None:
+        strides += (0, 0)
+        ptrs.append(0)
+    elif v.shape[1] != hkv:
+        raise ValueError("k and v must have the same number of heads")
+    for name, t, dt, n in (("positions", positions, torch.int32, tokens), ("inv_freq", inv_freq, torch.float32, None),
+                           ("q_weight", q_weight, torch.float32, HEAD_DIM),
+                           ("k_weight", k_weight, torch.float32, HEAD_DIM)):
+        if t is None and n == HEAD_DIM and dt is torch.float32:
+            continue
+        if t.dtype is not dt or t.get_device() != dev or not t.is_contiguous() or t.dim() != 1:
+            _need(t, dt, name)
+            raise ValueError(f"{name} must be one-dimensional on {q.device}")
+        if n is not None and t.shape[0] != n:
+            raise ValueError(f"{name} must have shape ({n},)")
+    a = _ROPE.pack(tokens, hq, hkv, HEAD_DIM, kind, 2 * inv_freq.shape[0], bool(interleaved), bool(norm), eps, rope_scale,
+                   *ptrs, *strides, positions.data_ptr(), inv_freq.data_ptr(), _ptr(q_weight), _ptr(k_weight),
+                   outs[0].data_ptr(), outs[1].data_ptr(), 0 if v is None else outs[2].data_ptr())
+    _run(q, stream, lib().okv_qk_norm_rope, a)
     return tuple(outs)
 
 
@@ -580,7 +584,6 @@ def dequantize(cache: Cache, seq_slot, block_table, context_lens, max_ctx: int, 
     if out is None:
         out = torch.empty((batch, cache.hkv, max_ctx, HEAD_DIM), dtype=torch.float32, device="cuda")
     desc = _desc_for(cache, out)
-    with _on(out):
-        _check(lib().okv_dequantize(ctypes.byref(desc), batch, _ptr(seq_slot), _ptr(block_table),
-                                    _ptr(context_lens), max_ctx, which, basis, source, _ptr(out), _stream(stream)))
+    _run(out, stream, lib().okv_dequantize, ctypes.byref(desc), batch, _ptr(seq_slot), _ptr(block_table),
+         _ptr(context_lens), max_ctx, which, basis, source, _ptr(out))
     return out
