@@ -207,7 +207,7 @@ okv_status okv_append_quantize(const okv_cache_desc* desc, const void* k, const 
 
 size_t okv_prefill_workspace_bytes(const okv_cache_desc* desc, int32_t T) {
   if (validate_desc(desc) != OKV_OK || T < 0) return 0;
-  return prefill_workspace_bytes(T, desc->num_q_heads);
+  return prefill_workspace_bytes(desc, T);
 }
 
 okv_status okv_prefill_attention(const okv_cache_desc* desc, const void* q, int32_t T, int32_t slot,
@@ -227,7 +227,7 @@ okv_status okv_prefill_attention(const okv_cache_desc* desc, const void* q, int3
   if ((long long)T * desc->num_q_heads > 0x7fffffffLL) return fail(OKV_ERR_INVALID_ARG, "T * Hq too large");
   if ((uintptr_t)q % 16 || (uintptr_t)out % (out_bf16(desc) ? 2 : 4) || (uintptr_t)workspace % 256)
     return fail(OKV_ERR_INVALID_ARG, "q must be 16-byte, out element and workspace 256-byte aligned");
-  const size_t need = prefill_workspace_bytes(T, desc->num_q_heads);
+  const size_t need = prefill_workspace_bytes(desc, T);
   if (workspace_bytes < need)
     return fail(OKV_ERR_INVALID_ARG, "workspace too small: %zu < %zu bytes", workspace_bytes, need);
   return launch_prefill(desc, q, T, slot, context_len, block_table, out, workspace, (cudaStream_t)stream);

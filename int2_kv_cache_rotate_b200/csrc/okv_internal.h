@@ -91,7 +91,7 @@ okv_status launch_decode_step(const okv_cache_desc* d, const void* k, const void
                               void* out, void* ws, const DecodePlan& plan, cudaStream_t s);
 okv_status launch_prefill(const okv_cache_desc* d, const void* q, int T, int slot, int context_len,
                           const int32_t* block_table, void* out, void* ws, cudaStream_t s);
-size_t prefill_workspace_bytes(int T, int hq);
+size_t prefill_workspace_bytes(const okv_cache_desc* d, int T);
 okv_status launch_dequant(const okv_cache_desc* d, int B, const int32_t* seq_slot,
                           const int32_t* block_table, const int32_t* context_lens, int max_ctx,
                           int which, int basis, int source, void* out, cudaStream_t s);

@@ -23,35 +23,17 @@
 //      dense contraction runs on the tensor cores; nothing is dequantised to
 //      a rounded value;
 //   3. normalise and un-rotate: o = (o' / l) R_V^T per row.
+#include <algorithm>
+
 #include "okv_common.cuh"
 #include "okv_internal.h"
+#include "prefill_common.cuh"
 #include "umma.cuh"
 
 namespace okv {
 namespace {
 
 constexpr int kPfRows = 128;  // query rows per attention CTA (the MMA's M)
-
-struct PrefillArgs {
-  const __nv_bfloat16* q;  // [T][Hq][128]
-  const int32_t* block_table;
-  const uint8_t* pages;
-  const __half* ring;
-  const __half* sink;
-  const float* u_k;
-  const float* u_v;
-  uint32_t* status;
-  __half* qhi;   // [T][Hq][128]: hi half of q~ 2^-e
-  __half* qlo;   // [T][Hq][128]: lo half
-  float* qaux;   // [T][Hq][8]: sum of q~ per group (4), 2^e, spare
-  float* obuf;   // [T][Hq][132]: o' (128), l, spare
-  void* out;     // [T][Hq][128], fp32 or bf16
-  int out_bf16;
-  int T, hq, hkv, g, ng, bhb, slot, L, first, mbps, num_blocks, nsink;
-};
-
-constexpr int kQaux = 8;
-constexpr int kOStride = 132;
 
 // ---------------------------------------------------------------------------
 // 1. q~ = q R_K for the chunk, and 3. o = (o' / l) R_V^T: one CTA per 64 rows
@@ -168,8 +150,17 @@ __global__ void __launch_bounds__(256) prefill_qrot_kernel(PrefillArgs a) {
         hw[f >> 1] = *reinterpret_cast<const uint32_t*>(&h);
         lw[f >> 1] = *reinterpret_cast<const uint32_t*>(&l2);
       }
-      *reinterpret_cast<uint2*>(a.qhi + (size_t)row * kD + 4 * r) = make_uint2(hw[0], hw[1]);
-      *reinterpret_cast<uint2*>(a.qlo + (size_t)row * kD + 4 * r) = make_uint2(lw[0], lw[1]);
+      if (a.q_order) {
+        // channels of eight in the order 0 4 1 5 2 6 3 7, hi half only (prefill_int4.cu): lane r
+        // holds channels 4 r .. + 3, the other four of its eight are lane r ^ 1's (lane ^ 16)
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, (r & 1) ? hw[0] : hw[1], 16);
+        const uint32_t lo4 = (r & 1) ? got : hw[0], hi4 = (r & 1) ? hw[1] : got;  // channels e, e + 1 of either half
+        *reinterpret_cast<uint2*>(a.qhi + (size_t)row * kD + 4 * r) =
+            make_uint2(__byte_perm(lo4, hi4, 0x5410u), __byte_perm(lo4, hi4, 0x7632u));
+      } else {
+        *reinterpret_cast<uint2*>(a.qhi + (size_t)row * kD + 4 * r) = make_uint2(hw[0], hw[1]);
+        *reinterpret_cast<uint2*>(a.qlo + (size_t)row * kD + 4 * r) = make_uint2(lw[0], lw[1]);
+      }
       // per-group sums of q~: channels 4r.. lie in group r ng / 32
       const float part = (zc[0] + zc[1]) + (zc[2] + zc[3]);
       float* aux = a.qaux + (size_t)row * kQaux;
@@ -1064,6 +1055,9 @@ __global__ void __launch_bounds__(kUpThreads, 1) prefill_umma_kernel(PrefillArgs
 // 3. o = (o' / l) R_V^T (see 1. for the tiling): un-permute, 1 / l and the
 // butterfly per row in registers, the row to shared memory, then o = x U_V^T
 // with U_V^T permuted: ut[i][4 l + j] = U_V[l + 32 j][i].
+// kSplit: o', l and the running maximum of a.splits key ranges per row are
+// merged first (ranges with l = 0 hold nothing and are not read).
+template <bool kSplit>
 __global__ void __launch_bounds__(256) prefill_unrotate_kernel(PrefillArgs a) {
   extern __shared__ __align__(16) float rt_[];
   float* ut = rt_;
@@ -1102,8 +1096,24 @@ __global__ void __launch_bounds__(256) prefill_unrotate_kernel(PrefillArgs a) {
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
     const float* src = a.obuf + (size_t)rt_row(a, hk, min(r0 + 8 * warp + k, nrows - 1)) * kOStride;
-    o4[k] = *reinterpret_cast<const float4*>(src + 4 * r);  // rotated channels 4 r .. 4 r + 3
-    lr[k] = src[128];
+    if constexpr (kSplit) {
+      const size_t next = (size_t)a.T * a.hq * kOStride;
+      // lane s holds (l, maximum) of range s (at most 32 ranges), then its weight 2^(m_s - m)
+      const float2 lm = lane < a.splits ? *reinterpret_cast<const float2*>(src + lane * next + 128) : make_float2(0.f, 0.f);
+      const float top = warp_max(lm.x > 0.f ? lm.y : -INFINITY);
+      const float w = lm.x > 0.f ? exp2f(lm.y - top) : 0.f;
+      lr[k] = warp_sum(w * lm.x);
+      o4[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int s = 0; s < a.splits; ++s) {
+        const float ws = __shfl_sync(0xffffffffu, w, s);
+        if (ws == 0.f) continue;
+        const float4 x = *reinterpret_cast<const float4*>(src + s * next + 4 * r);
+        o4[k] = make_float4(fmaf(ws, x.x, o4[k].x), fmaf(ws, x.y, o4[k].y), fmaf(ws, x.z, o4[k].z), fmaf(ws, x.w, o4[k].w));
+      }
+    } else {
+      o4[k] = *reinterpret_cast<const float4*>(src + 4 * r);  // rotated channels 4 r .. 4 r + 3
+      lr[k] = src[128];
+    }
   }
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
@@ -1144,13 +1154,24 @@ __global__ void __launch_bounds__(256) prefill_unrotate_kernel(PrefillArgs a) {
 
 }  // namespace
 
-size_t prefill_workspace_bytes(int T, int hq) {
-  const size_t rows = (size_t)T * hq;
+// Key ranges per row of the 4-bit kernel: as many as fill the GPU when the
+// chunk's row tiles do not (one CTA per SM), at most 32 (a warp's lanes in the
+// merge).  It depends on T alone, so that the workspace does.
+static int prefill_ranges(const okv_cache_desc* d, int T) {
+  if (code_bits(d) != 4 || T == 0) return 1;
+  const int sms = device_sm_count() > 0 ? device_sm_count() : 148;
+  const long long tiles = ((long long)T * (d->num_q_heads / d->num_kv_heads) + kP4Rows - 1) / kP4Rows;
+  const long long ctas = tiles * d->num_kv_heads;
+  return (int)std::max(1ll, std::min(32ll, sms / ctas));
+}
+
+size_t prefill_workspace_bytes(const okv_cache_desc* d, int T) {
+  const size_t rows = (size_t)T * d->num_q_heads;
   size_t off = 0;
   off += (rows * kD * sizeof(__half) + 255) / 256 * 256;  // qhi
   off += (rows * kD * sizeof(__half) + 255) / 256 * 256;  // qlo
   off += (rows * kQaux * sizeof(float) + 255) / 256 * 256;
-  off += (rows * kOStride * sizeof(float) + 255) / 256 * 256;
+  off += ((size_t)prefill_ranges(d, T) * rows * kOStride * sizeof(float) + 255) / 256 * 256;
   return off;
 }
 
@@ -1186,33 +1207,45 @@ okv_status launch_prefill(const okv_cache_desc* d, const void* q, int T, int slo
   a.slot = slot;
   a.L = context_len;
   a.first = context_len - T;
+  const bool int4_bf16 = code_bits(d) == 4 && a.out_bf16;  // prefill_int4.cu; else exact codes, two halves
+  a.q_order = int4_bf16;
   a.mbps = d->max_blocks_per_seq;
   a.num_blocks = d->num_blocks;
   a.nsink = d->num_sink;
-  static std::atomic<uint32_t> qr_attr{0}, ur_attr{0};
+  static std::atomic<uint32_t> qr_attr{0}, ur_attr{0}, us_attr{0};
   cudaError_t e0 = set_smem_limit_once((const void*)prefill_qrot_kernel, (int)kRtSmem, qr_attr);
-  if (e0 == cudaSuccess) e0 = set_smem_limit_once((const void*)prefill_unrotate_kernel, (int)kRtSmem, ur_attr);
+  if (e0 == cudaSuccess) e0 = set_smem_limit_once((const void*)prefill_unrotate_kernel<false>, (int)kRtSmem, ur_attr);
+  if (e0 == cudaSuccess) e0 = set_smem_limit_once((const void*)prefill_unrotate_kernel<true>, (int)kRtSmem, us_attr);
   if (e0 != cudaSuccess) return fail(OKV_ERR_CUDA, "prefill rotation smem attribute: %s", cudaGetErrorString(e0));
   const dim3 rt_grid((unsigned)((T * a.g + kRtRows - 1) / kRtRows), (unsigned)a.hkv);
   prefill_qrot_kernel<<<rt_grid, 256, kRtSmem, s>>>(a);
   okv_status st = check_launch("prefill query rotation");
   if (st != OKV_OK) return st;
-  const dim3 grid((unsigned)((T * a.g + kPfRows - 1) / kPfRows), (unsigned)a.hkv);
-  using Kernel = void (*)(PrefillArgs);
-  static const Kernel kernels[2][3] = {{prefill_umma_kernel<1, 2>, prefill_umma_kernel<2, 2>, prefill_umma_kernel<4, 2>},
-                                       {prefill_umma_kernel<1, 4>, prefill_umma_kernel<2, 4>, prefill_umma_kernel<4, 4>}};
-  static std::atomic<uint32_t> up_attr[2][3];  // per instantiation: ng = 1, 2, 4 -> 0, 1, 2
-  const int fi = code_bits(d) == 4, gi = a.ng >> 1;
-  const cudaError_t e1 = set_smem_limit_once((const void*)kernels[fi][gi], (int)kUpSmem, up_attr[fi][gi]);
-  if (e1 != cudaSuccess) return fail(OKV_ERR_CUDA, "prefill attention smem attribute: %s", cudaGetErrorString(e1));
-  kernels[fi][gi]<<<grid, kUpThreads, kUpSmem, s>>>(a);
-  st = check_launch("prefill attention");
+  a.splits = 1;
+  if (int4_bf16) {
+    // no more ranges than leave two chunks of 128 keys each
+    a.splits = std::max(1, std::min(prefill_ranges(d, T), (context_len + 255) / 256));
+    st = launch_prefill_int4_bf16(a, s);
+  } else {
+    const dim3 grid((unsigned)((T * a.g + kPfRows - 1) / kPfRows), (unsigned)a.hkv);
+    using Kernel = void (*)(PrefillArgs);
+    static const Kernel kernels[2][3] = {
+        {prefill_umma_kernel<1, 2>, prefill_umma_kernel<2, 2>, prefill_umma_kernel<4, 2>},
+        {prefill_umma_kernel<1, 4>, prefill_umma_kernel<2, 4>, prefill_umma_kernel<4, 4>}};
+    static std::atomic<uint32_t> up_attr[2][3];  // per instantiation: ng = 1, 2, 4 -> 0, 1, 2
+    const int fi = code_bits(d) == 4, gi = a.ng >> 1;
+    const cudaError_t e1 = set_smem_limit_once((const void*)kernels[fi][gi], (int)kUpSmem, up_attr[fi][gi]);
+    if (e1 != cudaSuccess) return fail(OKV_ERR_CUDA, "prefill attention smem attribute: %s", cudaGetErrorString(e1));
+    kernels[fi][gi]<<<grid, kUpThreads, kUpSmem, s>>>(a);
+    st = check_launch("prefill attention");
+  }
   if (st != OKV_OK) return st;
   // The un-rotation may start (programmatic launch) while the attention's last
   // CTAs run: it stages U_V, then waits for the attention's outputs.  Starting
   // the attention early behind the query rotation in the same way measured
   // slower with 64-channel groups (3.31 against 3.10 ms) and is not done.
-  const cudaError_t e3 = launch_pdl(prefill_unrotate_kernel, rt_grid, dim3(256), kRtSmem, s, true, a);
+  const cudaError_t e3 = launch_pdl(a.splits > 1 ? prefill_unrotate_kernel<true> : prefill_unrotate_kernel<false>,
+                                    rt_grid, dim3(256), kRtSmem, s, true, a);
   if (e3 != cudaSuccess) return fail(OKV_ERR_CUDA, "prefill un-rotation launch: %s", cudaGetErrorString(e3));
   return check_launch("prefill un-rotation");
 }
