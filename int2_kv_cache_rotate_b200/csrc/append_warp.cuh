@@ -1,7 +1,7 @@
 // Warp-level append shared by the append kernels and the fused decode-step
 // kernel: rotate (U, Hadamard butterfly, bit-reversal remap), quantise to INT2 or INT4
 // with fp16 scale/min, pack, and write the paged cache and the fp16 rows of
-// the recent-token window and of the sink tokens, for one 32-token tile of
+// the recent-token window and of the sink tokens, for one tile of tokens of
 // one (KV head, K|V).
 #pragma once
 
@@ -75,7 +75,7 @@ __device__ __forceinline__ __half* sink_row(const AppendArgs& a, int slot, int h
 
 constexpr int kAppThreads = 256;
 constexpr int kAppRound = 8;    // tokens reduced per round (one per warp)
-constexpr int kAppTokens = 32;  // tokens per CTA
+constexpr int kAppTokens = 8;   // tokens per CTA (one round; 32 made a 16-token step two rounds and 11.0 us, 8 makes it 7.0)
 
 // Validate token t's destination and write everything for one rotated vector.
 // Lane l owns pre-permutation channels l + 32a, which after P_br are rotated

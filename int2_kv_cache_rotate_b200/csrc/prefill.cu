@@ -43,29 +43,32 @@ constexpr int kPfRows = 128;  // query rows per attention CTA (the MMA's M)
 // U load feeds 8 rows, on the paired fp32 FMA.  The butterfly and the
 // bit-reversal remap run per row in registers.
 // ---------------------------------------------------------------------------
-constexpr int kRtRows = 64;
-constexpr size_t kRtSmem = (size_t)(kD * kD + kRtRows * kD) * sizeof(float);
+// Rows per warp: 8, or 2 where 64 rows per CTA would leave most SMs idle (203
+// tokens of 8 heads: 26 CTAs).
+__host__ __device__ constexpr int rt_rows(int rw) { return 8 * rw; }
+constexpr size_t rt_smem(int rw) { return (size_t)(kD * kD + rt_rows(rw) * kD) * sizeof(float); }
 
 // global row of row rk (0 .. T G - 1) of KV head hk: token rk / G, query head hk G + rk % G
 __device__ __forceinline__ int rt_row(const PrefillArgs& a, int hk, int rk) {
   return (rk / a.g) * a.hq + hk * a.g + rk % a.g;
 }
 
-// acc[rr] = x[rr] . U for 8 rows held in xs (fp32 rows of kD), U permuted in up
-__device__ __forceinline__ void rt_matvec8(const float* xs, const float* up, int lane, float2 (&acc)[8][2]) {
+// acc[rr] = x[rr] . U for RW rows held in xs (fp32 rows of kD), U permuted in up
+template <int RW>
+__device__ __forceinline__ void rt_matvec(const float* xs, const float* up, int lane, float2 (&acc)[RW][2]) {
 #pragma unroll
-  for (int rr = 0; rr < 8; ++rr) acc[rr][0] = acc[rr][1] = make_float2(0.f, 0.f);
+  for (int rr = 0; rr < RW; ++rr) acc[rr][0] = acc[rr][1] = make_float2(0.f, 0.f);
 #pragma unroll 1
   for (int i = 0; i < kD; i += 4) {
-    float4 x4[8];
+    float4 x4[RW];
 #pragma unroll
-    for (int rr = 0; rr < 8; ++rr) x4[rr] = *reinterpret_cast<const float4*>(xs + rr * kD + i);
+    for (int rr = 0; rr < RW; ++rr) x4[rr] = *reinterpret_cast<const float4*>(xs + rr * kD + i);
 #pragma unroll
     for (int ii = 0; ii < 4; ++ii) {
       const float4 u = *reinterpret_cast<const float4*>(up + (i + ii) * kD + 4 * lane);
       const float2 u01 = make_float2(u.x, u.y), u23 = make_float2(u.z, u.w);
 #pragma unroll
-      for (int rr = 0; rr < 8; ++rr) {
+      for (int rr = 0; rr < RW; ++rr) {
         const float xv = ii == 0 ? x4[rr].x : ii == 1 ? x4[rr].y : ii == 2 ? x4[rr].z : x4[rr].w;
         const float2 x2 = make_float2(xv, xv);
         acc[rr][0] = __ffma2_rn(x2, u01, acc[rr][0]);
@@ -75,7 +78,9 @@ __device__ __forceinline__ void rt_matvec8(const float* xs, const float* up, int
   }
 }
 
+template <int RW>
 __global__ void __launch_bounds__(256) prefill_qrot_kernel(PrefillArgs a) {
+  constexpr int kRtRows = rt_rows(RW);
   extern __shared__ __align__(16) float rt_[];
   float* up = rt_;             // up[i][4 l + c] = U_K[i][l + 32 c]
   float* xs = rt_ + kD * kD;   // the tile's query rows, fp32
@@ -117,11 +122,11 @@ __global__ void __launch_bounds__(256) prefill_qrot_kernel(PrefillArgs a) {
   }
   __syncthreads();
   {
-    const int rb = 8 * warp;
-    float2 acc[8][2];
-    rt_matvec8(xs + rb * kD, up, lane, acc);
+    const int rb = RW * warp;
+    float2 acc[RW][2];
+    rt_matvec<RW>(xs + rb * kD, up, lane, acc);
 #pragma unroll
-    for (int rr = 0; rr < 8; ++rr) {
+    for (int rr = 0; rr < RW; ++rr) {
       const int rk = r0 + rb + rr;
       if (rk >= nrows) continue;  // uniform across the warp
       const int row = rt_row(a, hk, rk);
@@ -1057,8 +1062,9 @@ __global__ void __launch_bounds__(kUpThreads, 1) prefill_umma_kernel(PrefillArgs
 // with U_V^T permuted: ut[i][4 l + j] = U_V[l + 32 j][i].
 // kSplit: o', l and the running maximum of a.splits key ranges per row are
 // merged first (ranges with l = 0 hold nothing and are not read).
-template <bool kSplit>
+template <bool kSplit, int RW>
 __global__ void __launch_bounds__(256) prefill_unrotate_kernel(PrefillArgs a) {
+  constexpr int kRtRows = rt_rows(RW);
   extern __shared__ __align__(16) float rt_[];
   float* ut = rt_;
   float* xs = rt_ + kD * kD;
@@ -1088,49 +1094,70 @@ __global__ void __launch_bounds__(256) prefill_unrotate_kernel(PrefillArgs a) {
     }
   }
   grid_dep_wait();  // the attention's outputs are read from here on
-  // this warp's 8 rows: x = H-butterfly of the un-permuted o' / l, into xs.
-  // All 8 rows' loads go out before the first butterfly.
+  // this warp's rows: x = H-butterfly of the un-permuted o' / l, into xs.
+  // All rows' loads go out before the first butterfly.
   const int r = rev5(lane);
-  float4 o4[8];
-  float lr[8];
+  float4 o4[RW];
+  float lr[RW];
+  const float* src[RW];
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const float* src = a.obuf + (size_t)rt_row(a, hk, min(r0 + 8 * warp + k, nrows - 1)) * kOStride;
-    if constexpr (kSplit) {
-      const size_t next = (size_t)a.T * a.hq * kOStride;
-      // lane s holds (l, maximum) of range s (at most 32 ranges), then its weight 2^(m_s - m)
-      const float2 lm = lane < a.splits ? *reinterpret_cast<const float2*>(src + lane * next + 128) : make_float2(0.f, 0.f);
-      const float top = warp_max(lm.x > 0.f ? lm.y : -INFINITY);
-      const float w = lm.x > 0.f ? exp2f(lm.y - top) : 0.f;
-      lr[k] = warp_sum(w * lm.x);
+  for (int k = 0; k < RW; ++k) src[k] = a.obuf + (size_t)rt_row(a, hk, min(r0 + RW * warp + k, nrows - 1)) * kOStride;
+  if constexpr (kSplit) {
+    // lane s holds (l, maximum) of range s (at most 32 ranges), then its weight 2^(m_s - m)
+    const size_t next = (size_t)a.T * a.hq * kOStride;
+    float w[RW];
+#pragma unroll
+    for (int k = 0; k < RW; ++k) {
+      const float2 lm =
+          lane < a.splits ? *reinterpret_cast<const float2*>(src[k] + lane * next + 128) : make_float2(0.f, 0.f);
+      lr[k] = lm.x;
+      w[k] = lm.y;
       o4[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int s = 0; s < a.splits; ++s) {
-        const float ws = __shfl_sync(0xffffffffu, w, s);
-        if (ws == 0.f) continue;
-        const float4 x = *reinterpret_cast<const float4*>(src + s * next + 4 * r);
-        o4[k] = make_float4(fmaf(ws, x.x, o4[k].x), fmaf(ws, x.y, o4[k].y), fmaf(ws, x.z, o4[k].z), fmaf(ws, x.w, o4[k].w));
+    }
+#pragma unroll
+    for (int k = 0; k < RW; ++k) {
+      const float top = warp_max(lr[k] > 0.f ? w[k] : -INFINITY);
+      w[k] = lr[k] > 0.f ? exp2f(w[k] - top) : 0.f;
+      lr[k] = warp_sum(w[k] * lr[k]);
+    }
+    // range by range, the warp's rows' loads in flight together (a row at
+    // a time, 18 ranges took 47 us)
+    for (int s = 0; s < a.splits; ++s) {
+      float4 x[RW];
+      float ws[RW];
+#pragma unroll
+      for (int k = 0; k < RW; ++k) {
+        ws[k] = __shfl_sync(0xffffffffu, w[k], s);
+        x[k] = ws[k] != 0.f ? *reinterpret_cast<const float4*>(src[k] + s * next + 4 * r) : make_float4(0.f, 0.f, 0.f, 0.f);
       }
-    } else {
-      o4[k] = *reinterpret_cast<const float4*>(src + 4 * r);  // rotated channels 4 r .. 4 r + 3
-      lr[k] = src[128];
+#pragma unroll
+      for (int k = 0; k < RW; ++k)
+        o4[k] = make_float4(fmaf(ws[k], x[k].x, o4[k].x), fmaf(ws[k], x[k].y, o4[k].y), fmaf(ws[k], x[k].z, o4[k].z),
+                            fmaf(ws[k], x[k].w, o4[k].w));
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < RW; ++k) {
+      o4[k] = *reinterpret_cast<const float4*>(src[k] + 4 * r);  // rotated channels 4 r .. 4 r + 3
+      lr[k] = src[k][128];
     }
   }
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
+  for (int k = 0; k < RW; ++k) {
     const float inv = lr[k] > 0.f ? 1.f / lr[k] : 0.f;
     // lane l: pre-permutation channels l + 32 aa = rotated channels 4 rev5(l) + rev2(aa)
     float y[4] = {o4[k].x * inv, o4[k].z * inv, o4[k].y * inv, o4[k].w * inv};
     wht128_warp(y, lane);
 #pragma unroll
-    for (int aa = 0; aa < 4; ++aa) xs[(8 * warp + k) * kD + lane + 32 * aa] = y[aa] * kInvSqrtD;
+    for (int aa = 0; aa < 4; ++aa) xs[(RW * warp + k) * kD + lane + 32 * aa] = y[aa] * kInvSqrtD;
   }
   __syncthreads();  // U_V^T staged (this warp's rows need only __syncwarp, U needs the CTA)
   {
-    const int rb = 8 * warp;
-    float2 acc[8][2];
-    rt_matvec8(xs + rb * kD, ut, lane, acc);
+    const int rb = RW * warp;
+    float2 acc[RW][2];
+    rt_matvec<RW>(xs + rb * kD, ut, lane, acc);
 #pragma unroll
-    for (int rr = 0; rr < 8; ++rr) {
+    for (int rr = 0; rr < RW; ++rr) {
       const int rk = r0 + rb + rr;
       if (rk < nrows) {
         const size_t at = (size_t)rt_row(a, hk, rk) * kD + lane;
@@ -1212,13 +1239,16 @@ okv_status launch_prefill(const okv_cache_desc* d, const void* q, int T, int slo
   a.mbps = d->max_blocks_per_seq;
   a.num_blocks = d->num_blocks;
   a.nsink = d->num_sink;
-  static std::atomic<uint32_t> qr_attr{0}, ur_attr{0}, us_attr{0};
-  cudaError_t e0 = set_smem_limit_once((const void*)prefill_qrot_kernel, (int)kRtSmem, qr_attr);
-  if (e0 == cudaSuccess) e0 = set_smem_limit_once((const void*)prefill_unrotate_kernel<false>, (int)kRtSmem, ur_attr);
-  if (e0 == cudaSuccess) e0 = set_smem_limit_once((const void*)prefill_unrotate_kernel<true>, (int)kRtSmem, us_attr);
+  const int sms = device_sm_count() > 0 ? device_sm_count() : 148;
+  const bool small = (long long)T * a.hq < 64ll * sms;  // fewer than one CTA of 64 rows per SM
+  const size_t rt_bytes = small ? rt_smem(2) : rt_smem(8);
+  const auto qrot = small ? prefill_qrot_kernel<2> : prefill_qrot_kernel<8>;
+  static std::atomic<uint32_t> qr_attr[2], ur_attr[2][2];
+  cudaError_t e0 = set_smem_limit_once((const void*)qrot, (int)rt_bytes, qr_attr[small]);
   if (e0 != cudaSuccess) return fail(OKV_ERR_CUDA, "prefill rotation smem attribute: %s", cudaGetErrorString(e0));
-  const dim3 rt_grid((unsigned)((T * a.g + kRtRows - 1) / kRtRows), (unsigned)a.hkv);
-  prefill_qrot_kernel<<<rt_grid, 256, kRtSmem, s>>>(a);
+  const int rt_cta_rows = small ? rt_rows(2) : rt_rows(8);
+  const dim3 rt_grid((unsigned)((T * a.g + rt_cta_rows - 1) / rt_cta_rows), (unsigned)a.hkv);
+  qrot<<<rt_grid, 256, rt_bytes, s>>>(a);
   okv_status st = check_launch("prefill query rotation");
   if (st != OKV_OK) return st;
   a.splits = 1;
@@ -1244,8 +1274,11 @@ okv_status launch_prefill(const okv_cache_desc* d, const void* q, int T, int slo
   // CTAs run: it stages U_V, then waits for the attention's outputs.  Starting
   // the attention early behind the query rotation in the same way measured
   // slower with 64-channel groups (3.31 against 3.10 ms) and is not done.
-  const cudaError_t e3 = launch_pdl(a.splits > 1 ? prefill_unrotate_kernel<true> : prefill_unrotate_kernel<false>,
-                                    rt_grid, dim3(256), kRtSmem, s, true, a);
+  const auto unrotate = a.splits > 1 ? (small ? prefill_unrotate_kernel<true, 2> : prefill_unrotate_kernel<true, 8>)
+                                     : (small ? prefill_unrotate_kernel<false, 2> : prefill_unrotate_kernel<false, 8>);
+  e0 = set_smem_limit_once((const void*)unrotate, (int)rt_bytes, ur_attr[a.splits > 1][small]);
+  if (e0 != cudaSuccess) return fail(OKV_ERR_CUDA, "prefill rotation smem attribute: %s", cudaGetErrorString(e0));
+  const cudaError_t e3 = launch_pdl(unrotate, rt_grid, dim3(256), rt_bytes, s, true, a);
   if (e3 != cudaSuccess) return fail(OKV_ERR_CUDA, "prefill un-rotation launch: %s", cudaGetErrorString(e3));
   return check_launch("prefill un-rotation");
 }

@@ -36,6 +36,8 @@
 // columns and in the value tile alike.
 // Bound: 128 keys x 256 rows cost 32 MMAs of 64 cycles and 32768 exponentials
 // at 16 a cycle, 2048 cycles each.
+#include <type_traits>
+
 #include "okv_common.cuh"
 #include "okv_internal.h"
 #include "prefill_common.cuh"
@@ -361,24 +363,32 @@ __global__ void __launch_bounds__(kP4Threads, 1) prefill_int4_kernel(PrefillArgs
       }
       {
         unsigned char* dst = gb + kP4OffK + (uint32_t)st * kP4Tile;
-        if (fk.src == 1) {
+        if (__builtin_expect(fk.src == 1, 1)) {
           bool big = false;  // |s c + m| may pass fp16's range
 #pragma unroll
-          for (int s = 0; s < 4; ++s) {
-            const __half2 sm = bits_h2(fk.sm[s * NG / 4]);
-            const __half2 s2 = __low2half2(sm), m2 = __high2half2(sm);
+          for (int k = 0; k < NG; ++k) {
+            const __half2 sm = bits_h2(fk.sm[k]);
             big = big || 15.f * __low2float(sm) + fabsf(__high2float(sm)) > 65504.f;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              // word s of chunk j: channels 32 s + 8 j .. + 7, low halves even
-              const uint32_t w = s == 0 ? fk.w[j].x : s == 1 ? fk.w[j].y : s == 2 ? fk.w[j].z : fk.w[j].w;
-              const uint32_t y = w >> 8;
-              uint4 o = make_uint4(p4_even(w, s2, m2), p4_odd(w, s2, m2), p4_even(y, s2, m2), p4_odd(y, s2, m2));
-              if (big) o = make_uint4(sat_h2(o.x), sat_h2(o.y), sat_h2(o.z), sat_h2(o.w));
-              *reinterpret_cast<uint4*>(dst + (s >> 1) * 16384 +
-                                        um_swz((uint32_t)krow, (uint32_t)(4 * (s & 1) + j) * 16u)) = o;
-            }
           }
+          auto convert = [&](auto sat) {
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+              const __half2 sm = bits_h2(fk.sm[s * NG / 4]);
+              const __half2 s2 = __low2half2(sm), m2 = __high2half2(sm);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                // word s of chunk j: channels 32 s + 8 j .. + 7, low halves even
+                const uint32_t w = s == 0 ? fk.w[j].x : s == 1 ? fk.w[j].y : s == 2 ? fk.w[j].z : fk.w[j].w;
+                const uint32_t y = w >> 8;
+                uint4 o = make_uint4(p4_even(w, s2, m2), p4_odd(w, s2, m2), p4_even(y, s2, m2), p4_odd(y, s2, m2));
+                if constexpr (decltype(sat)::value) o = make_uint4(sat_h2(o.x), sat_h2(o.y), sat_h2(o.z), sat_h2(o.w));
+                *reinterpret_cast<uint4*>(dst + (s >> 1) * 16384 +
+                                          um_swz((uint32_t)krow, (uint32_t)(4 * (s & 1) + j) * 16u)) = o;
+              }
+            }
+          };
+          if (__builtin_expect(big, 0)) convert(std::true_type{});
+          else convert(std::false_type{});
         } else {
           const uint4* x = fk.src == 2 ? reinterpret_cast<const uint4*>(fp16_row(kP4Keys * c + kt, 0)) : nullptr;
 #pragma unroll
@@ -410,34 +420,40 @@ __global__ void __launch_bounds__(kP4Threads, 1) prefill_int4_kernel(PrefillArgs
         auto put = [&](int ch, uint32_t t02, uint32_t t13) {  // the quad's four tokens of channel ch
           *reinterpret_cast<uint2*>(vdst + um_swz((uint32_t)ch, col)) = make_uint2(t02, t13);
         };
-        if (fv.src[bb] == 1) {
+        if (__builtin_expect(fv.src[bb] == 1, 1)) {
+          bool big = false;
 #pragma unroll
-          for (int k = 0; k < NG; ++k) {
-            const uint32_t q0 = pair_word(bb, 0, k), q1 = pair_word(bb, 1, k), q2 = pair_word(bb, 2, k),
-                           q3 = pair_word(bb, 3, k);
-            const __half2 s02 = bits_h2(__byte_perm(q0, q2, 0x5410u)), m02 = bits_h2(__byte_perm(q0, q2, 0x7632u));
-            const __half2 s13 = bits_h2(__byte_perm(q1, q3, 0x5410u)), m13 = bits_h2(__byte_perm(q1, q3, 0x7632u));
-            bool big = false;
+          for (int k = 0; k < NG; ++k)
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
-              const __half2 sm = bits_h2(t == 0 ? q0 : t == 1 ? q1 : t == 2 ? q2 : q3);
+              const __half2 sm = bits_h2(pair_word(bb, t, k));
               big = big || 15.f * __low2float(sm) + fabsf(__high2float(sm)) > 65504.f;
             }
+          auto convert = [&](auto sat) {
 #pragma unroll
-            for (int mt = 8 / NG * k; mt < 8 / NG * (k + 1); ++mt) {
-              const uint4& q = fv.w[bb][mt >> 2];
-              const uint32_t w = (mt & 3) == 0 ? q.x : (mt & 3) == 1 ? q.y : (mt & 3) == 2 ? q.z : q.w;
-              const uint32_t y = w >> 8;  // tokens 1 and 3
-              uint32_t e02 = p4_even(w, s02, m02), e13 = p4_even(y, s13, m13);
-              uint32_t o02 = p4_odd(w, s02, m02), o13 = p4_odd(y, s13, m13);
-              if (big) {
-                e02 = sat_h2(e02); e13 = sat_h2(e13);
-                o02 = sat_h2(o02); o13 = sat_h2(o13);
+            for (int k = 0; k < NG; ++k) {
+              const uint32_t q0 = pair_word(bb, 0, k), q1 = pair_word(bb, 1, k), q2 = pair_word(bb, 2, k),
+                             q3 = pair_word(bb, 3, k);
+              const __half2 s02 = bits_h2(__byte_perm(q0, q2, 0x5410u)), m02 = bits_h2(__byte_perm(q0, q2, 0x7632u));
+              const __half2 s13 = bits_h2(__byte_perm(q1, q3, 0x5410u)), m13 = bits_h2(__byte_perm(q1, q3, 0x7632u));
+#pragma unroll
+              for (int mt = 8 / NG * k; mt < 8 / NG * (k + 1); ++mt) {
+                const uint4& q = fv.w[bb][mt >> 2];
+                const uint32_t w = (mt & 3) == 0 ? q.x : (mt & 3) == 1 ? q.y : (mt & 3) == 2 ? q.z : q.w;
+                const uint32_t y = w >> 8;  // tokens 1 and 3
+                uint32_t e02 = p4_even(w, s02, m02), e13 = p4_even(y, s13, m13);
+                uint32_t o02 = p4_odd(w, s02, m02), o13 = p4_odd(y, s13, m13);
+                if constexpr (decltype(sat)::value) {
+                  e02 = sat_h2(e02); e13 = sat_h2(e13);
+                  o02 = sat_h2(o02); o13 = sat_h2(o13);
+                }
+                put(16 * mt + 2 * vg, e02, e13);
+                put(16 * mt + 2 * vg + 1, o02, o13);
               }
-              put(16 * mt + 2 * vg, e02, e13);
-              put(16 * mt + 2 * vg + 1, o02, o13);
             }
-          }
+          };
+          if (__builtin_expect(big, 0)) convert(std::true_type{});
+          else convert(std::false_type{});
         } else {
           const int p = quad_pos(c, bb);
           int src[4];
@@ -561,6 +577,7 @@ okv_status launch_prefill_int4_bf16(const PrefillArgs& a, cudaStream_t s) {
   const cudaError_t e = set_smem_limit_once((const void*)kernels[gi], (int)kP4Smem, attr[gi]);
   if (e != cudaSuccess) return fail(OKV_ERR_CUDA, "prefill attention smem attribute: %s", cudaGetErrorString(e));
   const dim3 grid((unsigned)((a.T * a.g + kP4Rows - 1) / kP4Rows), (unsigned)a.hkv, (unsigned)a.splits);
+  // (a programmatic launch behind the query rotation measured no faster: 885 against 871 us)
   kernels[gi]<<<grid, kP4Threads, kP4Smem, s>>>(a);
   return check_launch("prefill attention");
 }
