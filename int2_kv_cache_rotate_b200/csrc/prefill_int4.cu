@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(kP4Threads, 1) prefill_int4_kernel(PrefillArgs
     // ------------------------------------------------------------ softmax
     const uint32_t lb = (uint32_t)(32 * quarter) << 16;
     float m_use = -INFINITY;
-    float2 l2 = make_float2(0.f, 0.f);
+    float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};  // partial sums of the weights
     const float2 sc2 = make_float2(sc, sc);
     bool alive = tile < nt;
     for (int i = 0; i < n && alive; ++i) {
@@ -192,76 +192,77 @@ __global__ void __launch_bounds__(kP4Threads, 1) prefill_int4_kernel(PrefillArgs
       const int lim = min(rpos + 1, a.L) - kP4Keys * c;  // columns below it are visible
       const int* bd = ms.bad[c & 3];
       const bool bad = (bd[0] | bd[1] | bd[2] | bd[3]) != 0;
-      // two batches of 32 columns per round: the second's loads are in flight
-      // during the first (rolled up, so that the kernel's loops stay in the
-      // instruction cache together)
+      // A batch of 32 columns at a time, rolled up: the loops of the three roles
+      // share the instruction cache, and the smallest body was the fastest (one
+      // batch per turn 791 us a call, two with the second's loads ahead 806, all
+      // four unrolled 836; with the causal mask's selects inside, 860).
+      auto weights = [&](auto masked) {
 #pragma unroll 1
-      for (int b0 = 0; b0 < 4; b0 += 2) {
-      float v[2][32];
-      um_ld32(tS + lb + 32u * b0, v[0]);
+        for (int b = 0; b < 4; ++b) {
+          float x[32];
+          um_ld32(tS + lb + 32u * b, x);
+          um_wait_ld();
+          if constexpr (decltype(masked)::value) {
+            const int* kv = &ms.kval[c & 3][32 * b];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int b = b0 + h;
-        um_wait_ld();
-        if (h == 0) um_ld32(tS + lb + 32u * (b0 + 1), v[1]);
-        float* x = v[h];
-        if (__builtin_expect(lim < 32 * (b + 1) || bad, 0)) {
-          const int* kv = &ms.kval[c & 3][32 * b];
+            for (int j = 0; j < 32; ++j)
+              x[j] = (32 * b + swap_mid(j) < lim && (!bad || kv[j] != 0)) ? x[j] : -INFINITY;
+          }
+          float mx[2] = {fmaxf(x[0], x[1]), fmaxf(x[2], x[3])};
 #pragma unroll
-          for (int j = 0; j < 32; ++j)
-            x[j] = (32 * b + swap_mid(j) < lim && (!bad || kv[j] != 0)) ? x[j] : -INFINITY;
-        }
-        float mx[2] = {fmaxf(x[0], x[1]), fmaxf(x[2], x[3])};
-#pragma unroll
-        for (int j = 4; j < 32; j += 4) {
-          mx[0] = max3(mx[0], x[j], x[j + 1]);
-          mx[1] = max3(mx[1], x[j + 2], x[j + 3]);
-        }
-        const float bm = fmaxf(mx[0], mx[1]) * sc;
-        const bool need = bm > m_use + kP4Slack;
-        if (__any_sync(0xffffffffu, need)) {
-          // O_t holds every earlier chunk (S_t of this one was issued after its MMAs were done)
-          const float alpha = need ? p4_ex2(m_use - bm) : 1.f;  // 0 while the row has seen nothing
-          if (i > 0) {
+          for (int j = 4; j < 32; j += 4) {
+            mx[0] = max3(mx[0], x[j], x[j + 1]);
+            mx[1] = max3(mx[1], x[j + 2], x[j + 3]);
+          }
+          const float bm = fmaxf(mx[0], mx[1]) * sc;
+          const bool need = bm > m_use + kP4Slack;
+          if (__any_sync(0xffffffffu, need)) {
+            // O_t holds every earlier chunk (S_t of this one was issued after its MMAs were done)
+            const float alpha = need ? p4_ex2(m_use - bm) : 1.f;  // 0 while the row has seen nothing
+            if (i > 0) {
 #pragma unroll 1
-            for (int q = 0; q < 8; ++q) {
-              uint32_t o[16];
-              um_ld16(tO + lb + 16u * q, o);
+              for (int q = 0; q < 8; ++q) {
+                uint32_t o[16];
+                um_ld16(tO + lb + 16u * q, o);
+                um_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
+                um_st16(tO + lb + 16u * q, o);
+              }
+            }
+#pragma unroll 1
+            for (int q = 0; q < b; ++q) {  // weights of this chunk's batches before: columns 16 q ..
+              uint32_t u[16];
+              um_ld16(tS + lb + 16u * q, u);
               um_wait_ld();
 #pragma unroll
-              for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
-              um_st16(tO + lb + 16u * q, o);
+              for (int j = 0; j < 16; ++j) {
+                const float2 f = __half22float2(bits_h2(u[j]));
+                u[j] = h2_bits(__floats2half2_rn(f.x * alpha, f.y * alpha));
+              }
+              um_st16(tS + lb + 16u * q, u);
             }
+            um_wait_st();
+            ls[0] = __fmul2_rn(ls[0], make_float2(alpha, alpha));
+            ls[1] = __fmul2_rn(ls[1], make_float2(alpha, alpha));
+            if (need) m_use = bm;
           }
-#pragma unroll 1
-          for (int q = 0; q < b; ++q) {  // weights of this chunk's batches before: columns 16 q ..
-            uint32_t u[16];
-            um_ld16(tS + lb + 16u * q, u);
-            um_wait_ld();
+          const float nm = kP4Offset - (m_use == -INFINITY ? 0.f : m_use);
+          const float2 nm2 = make_float2(nm, nm);
+          uint32_t w[16];
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const float2 f = __half22float2(bits_h2(u[j]));
-              u[j] = h2_bits(__floats2half2_rn(f.x * alpha, f.y * alpha));
-            }
-            um_st16(tS + lb + 16u * q, u);
+          for (int j = 0; j < 16; ++j) {
+            const float2 d = __ffma2_rn(make_float2(x[2 * j], x[2 * j + 1]), sc2, nm2);
+            const float2 p = make_float2(p4_ex2(d.x), p4_ex2(d.y));
+            ls[j & 1] = __fadd2_rn(ls[j & 1], p);
+            w[j] = h2_bits(__floats2half2_rn(p.x, p.y));
           }
-          um_wait_st();
-          l2 = __fmul2_rn(l2, make_float2(alpha, alpha));
-          if (need) m_use = bm;
+          um_st16(tS + lb + 16u * b, w);
         }
-        const float nm = kP4Offset - (m_use == -INFINITY ? 0.f : m_use);
-        const float2 nm2 = make_float2(nm, nm);
-        uint32_t w[16];
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const float2 d = __ffma2_rn(make_float2(x[2 * j], x[2 * j + 1]), sc2, nm2);
-          const float2 p = make_float2(p4_ex2(d.x), p4_ex2(d.y));
-          l2 = __fadd2_rn(l2, p);
-          w[j] = h2_bits(__floats2half2_rn(p.x, p.y));
-        }
-        um_st16(tS + lb + 16u * b, w);
-      }
-      }
+      };
+      // (the whole warp one way: the bodies are warp-collective)
+      if (__builtin_expect(__any_sync(0xffffffffu, lim < kP4Keys || bad), 0)) weights(std::true_type{});
+      else weights(std::false_type{});
       um_wait_st();
       um_fence_before();
       mbar_arrive(&ms.p_full[tile]);
@@ -287,7 +288,7 @@ __global__ void __launch_bounds__(kP4Threads, 1) prefill_int4_kernel(PrefillArgs
         }
       }
       // a range without keys, or without a visible one, has l = 0 and is skipped by the merge
-      if (rok) *reinterpret_cast<float2*>(dst + 128) = make_float2(alive ? l2.x + l2.y : 0.f, m_use);
+      if (rok) *reinterpret_cast<float2*>(dst + 128) = make_float2(alive ? (ls[0].x + ls[0].y) + (ls[1].x + ls[1].y) : 0.f, m_use);
       if (!alive && lane == 0) raise_flag(a.status, OKV_DEV_TIMEOUT);
     }
   } else if (warp < 12) {
