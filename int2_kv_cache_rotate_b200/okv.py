@@ -179,6 +179,8 @@ def _run(t, stream, fn, *args):
 
 
 def _need(t, dtype, name, device=True):
+    if t is not None and t.dtype is dtype and t.is_contiguous() and (t.is_cuda or not device):
+        return t
     if t is None:
         raise ValueError(f"{name} is required")
     if t.dtype is not dtype:
@@ -188,6 +190,35 @@ def _need(t, dtype, name, device=True):
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t
+
+
+def _heads(t, dtype, name, heads):
+    """t: contiguous [rows][heads][128] on a GPU; returns its rows (none needs no shape)."""
+    _need(t, dtype, name)
+    shape = t.shape
+    if len(shape) == 3 and shape[1] == heads and shape[2] == HEAD_DIM:
+        return shape[0]
+    if t.numel() == 0:
+        return 0
+    raise ValueError(f"{name} must be [rows][{heads}][{HEAD_DIM}], got {tuple(shape)}")
+
+
+def _ints(t, name, least):
+    """t: contiguous int32 on a GPU with `least` values or more."""
+    if t is not None and t.dtype is _torch.int32 and t.is_cuda and t.is_contiguous() and t.numel() >= least:
+        return t.data_ptr()
+    _need(t, _t().int32, name)
+    raise ValueError(f"{name} must hold at least {least} values, got {t.numel()}")
+
+
+def _out(cache, out, rows, device):
+    """The output of `rows` query rows (a new fp32 tensor when None) and the descriptor that writes its type."""
+    if out is None:
+        return _torch.empty((rows, cache.hq, HEAD_DIM), dtype=_torch.float32, device=device), cache.desc
+    desc = _desc_for(cache, out)
+    if out.numel() < rows * cache.hq * HEAD_DIM:
+        raise ValueError(f"out must hold [{rows}][{cache.hq}][{HEAD_DIM}] values, got {tuple(out.shape)}")
+    return out, desc
 
 
 # ---------------------------------------------------------------- calibration
@@ -298,16 +329,20 @@ def load_rotations(path, verify: bool = True) -> dict:
 
 def append_quantize(cache: Cache, k, v, seq_slot, pos, block_table, slot_lens, pre_rotated=False,
                     rotated_out=None, stream=None):
-    import torch
+    torch = _t()
     dt = torch.float32 if pre_rotated else torch.bfloat16
-    _need(k, dt, "k"), _need(v, dt, "v")
-    for name, t in (("seq_slot", seq_slot), ("pos", pos), ("block_table", block_table), ("slot_lens", slot_lens)):
-        _need(t, torch.int32, name)
+    T = _heads(k, dt, "k", cache.hkv)
+    if _heads(v, dt, "v", cache.hkv) != T:
+        raise ValueError("k and v must have the same number of rows")
     if rotated_out is not None:
         _need(rotated_out, torch.float32, "rotated_out")
-    T = k.shape[0] if k.dim() > 0 else 0
-    _run(k, stream, lib().okv_append_quantize, ctypes.byref(cache.desc), _ptr(k), _ptr(v), T, _ptr(seq_slot),
-         _ptr(pos), _ptr(block_table), _ptr(slot_lens), PRE_ROTATED if pre_rotated else 0, _ptr(rotated_out))
+        if rotated_out.numel() < 2 * k.numel():
+            raise ValueError("rotated_out must hold [T][2][Hkv][128] values")
+    slots = cache.num_seq_slots if T else 0
+    _run(k, stream, lib().okv_append_quantize, ctypes.byref(cache.desc), k.data_ptr(), v.data_ptr(), T,
+         _ints(seq_slot, "seq_slot", T), _ints(pos, "pos", T),
+         _ints(block_table, "block_table", slots * cache.max_blocks_per_seq), _ints(slot_lens, "slot_lens", slots),
+         PRE_ROTATED if pre_rotated else 0, _ptr(rotated_out))
 
 
 def decode_workspace_bytes(cache: Cache, batch: int) -> int:
@@ -315,44 +350,56 @@ def decode_workspace_bytes(cache: Cache, batch: int) -> int:
 
 
 def workspace(cache: Cache, batch: int):
-    import torch
-    return torch.empty(max(decode_workspace_bytes(cache, batch), 256), dtype=torch.uint8, device="cuda")
+    return _t().empty(max(decode_workspace_bytes(cache, batch), 256), dtype=_torch.uint8, device=cache.pages.device)
+
+
+def _decode_args(cache, q, seq_slot, block_table, context_lens):
+    """Rows of q, and the pointers of a decode call's integer arrays."""
+    B = _heads(q, _t().bfloat16, "q", cache.hq)
+    slots = cache.num_seq_slots if B else 0
+    return (B, _ints(seq_slot, "seq_slot", B), _ints(block_table, "block_table", slots * cache.max_blocks_per_seq),
+            _ints(context_lens, "context_lens", B))
 
 
 def decode_attention(cache: Cache, q, seq_slot, block_table, context_lens, out=None, ws=None, stream=None):
-    torch = _t()
-    _need(q, torch.bfloat16, "q")
-    for name, t in (("seq_slot", seq_slot), ("block_table", block_table), ("context_lens", context_lens)):
-        _need(t, torch.int32, name)
-    batch = q.shape[0]
-    if out is None:
-        out = torch.empty((batch, cache.hq, HEAD_DIM), dtype=torch.float32, device=q.device)
-    desc = _desc_for(cache, out)
+    """Decode attention of one query per sequence; out: fp32 (a new tensor when None) or bf16 [B, Hq, 128]."""
+    B, seq, table, ctx = _decode_args(cache, q, seq_slot, block_table, context_lens)
+    out, desc = _out(cache, out, B, q.device)
     if ws is None:
-        ws = workspace(cache, batch)
-    _run(q, stream, lib().okv_decode_attention, ctypes.byref(desc), _ptr(q), batch, _ptr(seq_slot),
-         _ptr(block_table), _ptr(context_lens), _ptr(out), _ptr(ws), ws.numel())
+        ws = workspace(cache, B)
+    _run(q, stream, lib().okv_decode_attention, ctypes.byref(desc), q.data_ptr(), B, seq, table, ctx, out.data_ptr(),
+         ws.data_ptr(), ws.numel())
     return out
+
+
+def _step_args(cache, k, v, new_seq_slot, new_pos, slot_lens, q, seq_slot, block_table, context_lens, out, ws):
+    """Output, the library's arguments but for the stream, and what they point into."""
+    bf16 = _t().bfloat16
+    _need(k, bf16, "k"), _need(v, bf16, "v"), _need(q, bf16, "q")
+    for name, t in (("new_seq_slot", new_seq_slot), ("new_pos", new_pos), ("slot_lens", slot_lens)):
+        _need(t, _torch.int32, name)
+    B, seq, table, ctx = _decode_args(cache, q, seq_slot, block_table, context_lens)
+    T = _heads(k, bf16, "k", cache.hkv)
+    if _heads(v, bf16, "v", cache.hkv) != T:
+        raise ValueError("k and v must have the same number of rows")
+    slots = cache.num_seq_slots if T else 0
+    if T and not B:
+        _ints(block_table, "block_table", slots * cache.max_blocks_per_seq)
+    out, desc = _out(cache, out, B, q.device)
+    if ws is None:
+        ws = workspace(cache, B)
+    args = (ctypes.byref(desc), k.data_ptr(), v.data_ptr(), T, _ints(new_seq_slot, "new_seq_slot", T),
+            _ints(new_pos, "new_pos", T), _ints(slot_lens, "slot_lens", slots), q.data_ptr(), B, seq, table, ctx,
+            out.data_ptr(), ws.data_ptr(), ws.numel())
+    return out, args, (desc, ws)
 
 
 def decode_step(cache: Cache, k, v, new_seq_slot, new_pos, slot_lens, q, seq_slot, block_table, context_lens,
                 out=None, ws=None, stream=None):
-    """Append this step's bf16 tokens, then decode (one call; see okv_decode_step)."""
-    torch = _t()
-    _need(k, torch.bfloat16, "k"), _need(v, torch.bfloat16, "v"), _need(q, torch.bfloat16, "q")
-    for name, t in (("new_seq_slot", new_seq_slot), ("new_pos", new_pos), ("slot_lens", slot_lens),
-                    ("seq_slot", seq_slot), ("block_table", block_table), ("context_lens", context_lens)):
-        _need(t, torch.int32, name)
-    B = q.shape[0]
-    T = k.shape[0]
-    if out is None:
-        out = torch.empty((B, cache.hq, HEAD_DIM), dtype=torch.float32, device=q.device)
-    desc = _desc_for(cache, out)
-    if ws is None:
-        ws = workspace(cache, B)
-    _run(q, stream, lib().okv_decode_step, ctypes.byref(desc), _ptr(k), _ptr(v), T, _ptr(new_seq_slot),
-         _ptr(new_pos), _ptr(slot_lens), _ptr(q), B, _ptr(seq_slot), _ptr(block_table), _ptr(context_lens), _ptr(out),
-         _ptr(ws), ws.numel())
+    """Append this step's bf16 tokens, then decode (one call; see okv_decode_step); out: fp32 or bf16 [B, Hq, 128]."""
+    out, args, _ = _step_args(cache, k, v, new_seq_slot, new_pos, slot_lens, q, seq_slot, block_table, context_lens,
+                              out, ws)
+    _run(q, stream, lib().okv_decode_step, *args)
     return out
 
 
@@ -367,24 +414,11 @@ class DecodeStepCall:
 
     def __init__(self, cache: Cache, k, v, new_seq_slot, new_pos, slot_lens, q, seq_slot, block_table,
                  context_lens, out=None, ws=None, stream=None, graph: bool = False):
-        import torch
-        _need(k, torch.bfloat16, "k"), _need(v, torch.bfloat16, "v"), _need(q, torch.bfloat16, "q")
-        for name, t in (("new_seq_slot", new_seq_slot), ("new_pos", new_pos), ("slot_lens", slot_lens),
-                        ("seq_slot", seq_slot), ("block_table", block_table), ("context_lens", context_lens)):
-            _need(t, torch.int32, name)
-        B = q.shape[0]
-        if out is None:
-            out = torch.empty((B, cache.hq, HEAD_DIM), dtype=torch.float32, device=q.device)
-        desc = _desc_for(cache, out)
-        if ws is None:
-            ws = workspace(cache, B)
-        self.out, self._keep = out, (cache, desc, k, v, new_seq_slot, new_pos, slot_lens, q, seq_slot, block_table,
-                                      context_lens, ws)
+        self.out, self._args, keep = _step_args(cache, k, v, new_seq_slot, new_pos, slot_lens, q, seq_slot, block_table,
+                                                context_lens, out, ws)
+        self._keep = (cache, k, v, new_seq_slot, new_pos, slot_lens, q, seq_slot, block_table, context_lens, keep)
         self._fn = lib().okv_decode_step
         self._stream = stream
-        self._args = (ctypes.byref(desc), _ptr(k), _ptr(v), k.shape[0], _ptr(new_seq_slot), _ptr(new_pos),
-                      _ptr(slot_lens), _ptr(q), B, _ptr(seq_slot), _ptr(block_table), _ptr(context_lens), _ptr(out),
-                      _ptr(ws), ws.numel())
         self._want_graph, self._graph = graph, None
 
     def __call__(self):
@@ -413,16 +447,10 @@ class DecodeStepCall:
 
 def decode_attention_noalloc(cache: Cache, q, seq_slot, block_table, context_lens, out=None, stream=None):
     """Decode attention with the library's static scratch (no workspace, no allocation in the library)."""
-    torch = _t()
-    _need(q, torch.bfloat16, "q")
-    for name, t in (("seq_slot", seq_slot), ("block_table", block_table), ("context_lens", context_lens)):
-        _need(t, torch.int32, name)
-    batch = q.shape[0]
-    if out is None:
-        out = torch.empty((batch, cache.hq, HEAD_DIM), dtype=torch.float32, device=q.device)
-    desc = _desc_for(cache, out)
-    _run(q, stream, lib().okv_decode_attention_noalloc, ctypes.byref(desc), _ptr(q), batch, _ptr(seq_slot),
-         _ptr(block_table), _ptr(context_lens), _ptr(out))
+    B, seq, table, ctx = _decode_args(cache, q, seq_slot, block_table, context_lens)
+    out, desc = _out(cache, out, B, q.device)
+    _run(q, stream, lib().okv_decode_attention_noalloc, ctypes.byref(desc), q.data_ptr(), B, seq, table, ctx,
+         out.data_ptr())
     return out
 
 
@@ -432,18 +460,15 @@ def prefill_workspace_bytes(cache: Cache, T: int) -> int:
 
 def prefill_attention(cache: Cache, q, slot: int, context_len: int, block_table, out=None, ws=None, stream=None):
     """Causal attention of a prefill chunk (q: bf16 [T, Hq, 128], already appended at positions
-    context_len - T .. context_len - 1 of sequence `slot`) over the cache; returns fp32 [T, Hq, 128]."""
-    torch = _t()
-    _need(q, torch.bfloat16, "q")
-    _need(block_table, torch.int32, "block_table")
-    T = q.shape[0]
-    if out is None:
-        out = torch.empty((T, cache.hq, HEAD_DIM), dtype=torch.float32, device=q.device)
-    desc = _desc_for(cache, out)
+    context_len - T .. context_len - 1 of sequence `slot`) over the cache; returns [T, Hq, 128] in fp32 (a new tensor
+    when out is None) or in out's type, fp32 or bf16."""
+    T = _heads(q, _t().bfloat16, "q", cache.hq)
+    table = _ints(block_table, "block_table", cache.num_seq_slots * cache.max_blocks_per_seq if T else 0)
+    out, desc = _out(cache, out, T, q.device)
     if ws is None:
-        ws = torch.empty(max(prefill_workspace_bytes(cache, T), 256), dtype=torch.uint8, device=q.device)
-    _run(q, stream, lib().okv_prefill_attention, ctypes.byref(desc), _ptr(q), T, int(slot), int(context_len),
-         _ptr(block_table), _ptr(out), _ptr(ws), ws.numel())
+        ws = _torch.empty(max(prefill_workspace_bytes(cache, T), 256), dtype=_torch.uint8, device=q.device)
+    _run(q, stream, lib().okv_prefill_attention, ctypes.byref(desc), q.data_ptr(), T, int(slot), int(context_len),
+         table, out.data_ptr(), ws.data_ptr(), ws.numel())
     return out
 
 
@@ -519,52 +544,58 @@ def qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps: f
     rows on 16-byte boundaries); positions int32 [T] (negative: a padding row, left as it is); inv_freq fp32
     [rot_dim/2]; weights fp32 [128].  Returns contiguous bf16 (q, k), or (q, k, v) when v is given."""
     torch = _t()
-    kind = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}.get(q.dtype)
-    if kind is None:
-        raise TypeError(f"q must be bfloat16, float16 or float32, got {q.dtype}")
-    given = (("q", q, q_out), ("k", k, k_out)) if v is None else (("q", q, q_out), ("k", k, k_out), ("v", v, v_out))
-    for name, t, _ in given:
-        if t.dtype is not q.dtype:
-            raise TypeError(f"{name} must be {q.dtype} like q, got {t.dtype}")
-    dev = q.get_device()
-    strides, ptrs, outs = [], [], []
-    for name, t, out in given:
+    bf16, dt, dev = torch.bfloat16, q.dtype, q.get_device()
+    kind = 0 if dt is bf16 else 1 if dt is torch.float16 else 2 if dt is torch.float32 else -1
+    if kind < 0:
+        raise TypeError(f"q must be bfloat16, float16 or float32, got {dt}")
+    for name, t in (("k", k), ("v", v)):
+        if t is not None and t.dtype is not dt:
+            raise TypeError(f"{name} must be {dt} like q, got {t.dtype}")
+
+    def view(t, name):  # rows of 128, heads and tokens at any stride
+        shape, st = t.shape, t.stride()
         if dev < 0 or t.get_device() != dev:
             raise ValueError(f"{name} must be a CUDA tensor on one device with q")
-        shape, st = t.shape, t.stride()
-        if len(shape) != 3 or shape[0] != q.shape[0] or shape[2] != HEAD_DIM or st[2] != 1:
+        if len(shape) != 3 or shape[2] != HEAD_DIM or st[2] != 1 or shape[0] != tokens:
             raise ValueError(f"{name} must be [T][heads][{HEAD_DIM}] with contiguous rows, got {tuple(shape)}")
-        strides += st[:2]
-        ptrs.append(t.data_ptr())
-        if out is None:
-            out = torch.empty(shape, dtype=torch.bfloat16, device=t.device)
-        elif out.dtype is not torch.bfloat16 or out.shape != shape or out.get_device() != dev or \
-                not out.is_contiguous():
-            _need(out, torch.bfloat16, name + "_out")
-            raise ValueError(f"{name}_out must have shape {tuple(shape)} on {q.device}")
-        outs.append(out)
-    tokens, hq, _ = q.shape
-    hkv = k.shape[1]
-    if v is None:
-        strides += (0, 0)
-        ptrs.append(0)
-    elif v.shape[1] != hkv:
-        raise ValueError("k and v must have the same number of heads")
-    for name, t, dt, n in (("positions", positions, torch.int32, tokens), ("inv_freq", inv_freq, torch.float32, None),
-                           ("q_weight", q_weight, torch.float32, HEAD_DIM),
-                           ("k_weight", k_weight, torch.float32, HEAD_DIM)):
-        if t is None and n == HEAD_DIM and dt is torch.float32:
-            continue
-        if t.dtype is not dt or t.get_device() != dev or not t.is_contiguous() or t.dim() != 1:
-            _need(t, dt, name)
+        return shape, st
+
+    def result(t, shape, name):
+        if t is None:
+            return torch.empty(shape, dtype=bf16, device=q.device)
+        if t.dtype is not bf16 or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+            _need(t, bf16, name)
+            raise ValueError(f"{name} must have shape {tuple(shape)} on {q.device}")
+        return t
+
+    def small(t, want, name, n):
+        if t is None or t.dtype is not want or t.get_device() != dev or not t.is_contiguous() or t.dim() != 1:
+            _need(t, want, name)
             raise ValueError(f"{name} must be one-dimensional on {q.device}")
-        if n is not None and t.shape[0] != n:
+        if n >= 0 and t.shape[0] != n:
             raise ValueError(f"{name} must have shape ({n},)")
-    a = _ROPE.pack(tokens, hq, hkv, HEAD_DIM, kind, 2 * inv_freq.shape[0], bool(interleaved), bool(norm), eps, rope_scale,
-                   *ptrs, *strides, positions.data_ptr(), inv_freq.data_ptr(), _ptr(q_weight), _ptr(k_weight),
-                   outs[0].data_ptr(), outs[1].data_ptr(), 0 if v is None else outs[2].data_ptr())
+        return t.data_ptr()
+
+    tokens = q.shape[0] if q.dim() else -1
+    (qs, qst), (ks, kst) = view(q, "q"), view(k, "k")
+    q_out, k_out = result(q_out, qs, "q_out"), result(k_out, ks, "k_out")
+    if v is not None:
+        vs, (vt, vh, _) = view(v, "v")
+        if vs[1] != ks[1]:
+            raise ValueError("k and v must have the same number of heads")
+        v_out = result(v_out, vs, "v_out")
+        vp, vo = v.data_ptr(), v_out.data_ptr()
+    else:
+        vp = vo = vt = vh = 0
+    f32 = torch.float32
+    a = _ROPE.pack(tokens, qs[1], ks[1], HEAD_DIM, kind, 0 if inv_freq is None else 2 * inv_freq.numel(),
+                   bool(interleaved), bool(norm), eps, rope_scale, q.data_ptr(), k.data_ptr(), vp, qst[0], qst[1],
+                   kst[0], kst[1], vt, vh, small(positions, torch.int32, "positions", tokens),
+                   small(inv_freq, f32, "inv_freq", -1), 0 if q_weight is None else small(q_weight, f32, "q_weight", HEAD_DIM),
+                   0 if k_weight is None else small(k_weight, f32, "k_weight", HEAD_DIM), q_out.data_ptr(),
+                   k_out.data_ptr(), vo)
     _run(q, stream, lib().okv_qk_norm_rope, a)
-    return tuple(outs)
+    return (q_out, k_out) if v is None else (q_out, k_out, v_out)
 
 
 def time_next_decode_kernel(start_event, stop_event):
@@ -577,13 +608,17 @@ def time_next_decode_kernel(start_event, stop_event):
 
 def dequantize(cache: Cache, seq_slot, block_table, context_lens, max_ctx: int, which: int, basis: int = 0,
                source: int = 0, out=None, stream=None):
-    import torch
+    torch = _t()
     for name, t in (("seq_slot", seq_slot), ("block_table", block_table), ("context_lens", context_lens)):
         _need(t, torch.int32, name)
     batch = seq_slot.shape[0]
     if out is None:
-        out = torch.empty((batch, cache.hkv, max_ctx, HEAD_DIM), dtype=torch.float32, device="cuda")
+        out = torch.empty((batch, cache.hkv, max_ctx, HEAD_DIM), dtype=torch.float32, device=seq_slot.device)
     desc = _desc_for(cache, out)
-    _run(out, stream, lib().okv_dequantize, ctypes.byref(desc), batch, _ptr(seq_slot), _ptr(block_table),
-         _ptr(context_lens), max_ctx, which, basis, source, _ptr(out))
+    if out.numel() < batch * cache.hkv * max(max_ctx, 0) * HEAD_DIM:
+        raise ValueError(f"out must hold [{batch}][{cache.hkv}][{max_ctx}][{HEAD_DIM}] values, got {tuple(out.shape)}")
+    slots = cache.num_seq_slots if batch else 0
+    _run(out, stream, lib().okv_dequantize, ctypes.byref(desc), batch, seq_slot.data_ptr(),
+         _ints(block_table, "block_table", slots * cache.max_blocks_per_seq), _ints(context_lens, "context_lens", batch),
+         max_ctx, which, basis, source, out.data_ptr())
     return out
