@@ -114,6 +114,17 @@ typedef enum {
 #define OKV_INT4 0x10000     /* 4-bit codes (else 2-bit)                     */
 #define OKV_OUT_BF16 0x20000 /* attention and dequantise outputs are bf16    */
 #define OKV_PAD_ROWS 0x40000 /* appended rows whose slot is -1 are padding   */
+/* OKV_OUT_BF16: `out` of okv_decode_attention, okv_decode_step,
+ * okv_decode_attention_noalloc, okv_prefill_attention and okv_dequantize is
+ * bf16 instead of fp32, 2-byte aligned (16 for okv_dequantize).  A decode or
+ * gather rounds the same fp32 result once.  A prefill over 4-bit codes then
+ * also reads q~, the dequantised keys and values (saturating at +-65504, like
+ * the cache's fp16 rows) and the softmax weights as fp16, each rounded once:
+ * one matrix product where fp32 output takes two.  It is a property of the
+ * call, not of the cache: the same buffers serve both.
+ * OKV_PAD_ROWS: appended rows (and gathered sequences) whose sequence slot is
+ * exactly -1 are skipped without OKV_DEV_BAD_SLOT, as okv_plan_append leaves
+ * them behind the last token. */
 
 #define OKV_HEAD_DIM 128
 #define OKV_BLOCK_TOKENS 16
@@ -324,7 +335,9 @@ okv_status okv_decode_attention_noalloc(const okv_cache_desc* desc, const void* 
  *   q: device bf16 [T][Hq][d], 16-byte aligned; slot, context_len: host ints (T <= L <=
  *   max_blocks_per_seq * 16); block_table: device, as above; out: device
  *   fp32 [T][Hq][d]; workspace: device, at least
- *   okv_prefill_workspace_bytes(desc, T) bytes, 256-B aligned.
+ *   okv_prefill_workspace_bytes(desc, T) bytes, 256-B aligned (the same for
+ *   either output type; a short chunk over 4-bit codes is split over key
+ *   ranges, whose partial results it holds).
  * Three launches on `stream` (query rotation, attention on the tensor cores,
  * normalisation and value un-rotation).  Errors: INVALID_ARG (NULL, sizes,
  * slot or context_len out of range, workspace too small); block ids outside

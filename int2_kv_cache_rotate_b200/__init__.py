@@ -1,4 +1,4 @@
-"""B200-native INT2 KV cache with attention-aware rotations (OSCAR-style).
+"""B200-native INT2 / INT4 KV cache with attention-aware rotations (OSCAR-style).
 
 The compute path is the C-ABI library ``libokv.so`` built from ``csrc/``;
 ``okv`` is its thin ctypes binding.  Importing the package does not load the

@@ -1,6 +1,6 @@
-// Decode attention over the INT2 paged cache: query rotation, split-K
-// attention with online softmax, and the split combine with the value
-// un-rotation.
+// Decode attention over the paged INT2 or INT4 cache: query rotation, split-K
+// attention with online softmax (decode_heads.cuh; here its CUDA-core form for
+// other KV head counts), and the split combine with the value un-rotation.
 #include "append_warp.cuh"
 #include "decode_heads.cuh"
 #include "okv_common.cuh"
