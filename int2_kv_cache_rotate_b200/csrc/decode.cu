@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(kPrepThreads) qrot_kernel(DecodeArgs a) {
 }
 
 // One launch for the start of a decode step: CTAs [0, n_app) append the
-// step's new tokens (one 32-token tile of one (KV head, K|V) each), the rest
+// step's new tokens (one 8-token tile of one (KV head, K|V) each), the rest
 // rotate the queries.  The two halves touch disjoint data.
 __global__ void __launch_bounds__(kPrepThreads) step_prep_kernel(AppendArgs aa, int T, int n_tiles, DecodeArgs a) {
   grid_dep_launch();

@@ -316,7 +316,7 @@ __global__ void __launch_bounds__(kP4Threads, 1) prefill_int4_kernel(PrefillArgs
     // values: thread = (token quad, code byte mod 8) of two blocks
     const int vg = lane >> 2, tq = lane & 3, vw = warp - 8;  // blocks 2 vw, 2 vw + 1 of the chunk
     struct FetchedV {
-      int src[2];       // per block: 1 all four tokens from codes, 0 none read, 3 sorted token by token
+      int src[2];       // per block: 1 all four tokens from codes, 0 none read, else token by token (2: no codes)
       uint4 w[2][2];    // words 0-3 and 4-7: byte 8 mt + vg of tokens 4 tq .. + 3
       uint4 sm[2][NG];  // (scale, min) of the four tokens, NG pairs each
     } fv;
@@ -335,7 +335,8 @@ __global__ void __launch_bounds__(kP4Threads, 1) prefill_int4_kernel(PrefillArgs
         const int p = quad_pos(c, bb);
         const int first = source(p, blk[bb]), last = p + 3 > pmax || p + 3 >= a.L ? 0 : source(p + 3, blk[bb]);
         // a quad lies on one side of the sinks' end (a multiple of 16); only the window's start and pmax cut it
-        fv.src[bb] = first == 1 && last == 1 ? 1 : first == 0 ? 0 : 3;
+        // (a bad block id skips the quad's code positions; window positions in it are still read)
+        fv.src[bb] = first == 1 && last == 1 ? 1 : first == 1 ? 3 : first == 2 || last == 2 ? 2 : 0;
         if (first == 1) fetch_block(head_of(blk[bb]), bb);
       }
     };
@@ -461,7 +462,10 @@ __global__ void __launch_bounds__(kP4Threads, 1) prefill_int4_kernel(PrefillArgs
 #pragma unroll
           for (int t = 0; t < 4; ++t) {
             const int pt = p + t;
-            src[t] = fv.src[bb] == 0 || pt > pmax || pt >= a.L ? 0 : (pt < a.nsink || pt >= a.L - kWin) ? 2 : 1;
+            src[t] = fv.src[bb] == 0 || pt > pmax || pt >= a.L        ? 0
+                     : (pt < a.nsink || pt >= a.L - kWin) ? 2
+                     : fv.src[bb] == 3                    ? 1
+                                                          : 0;
           }
 #pragma unroll
           for (int mt = 0; mt < 8; ++mt) {

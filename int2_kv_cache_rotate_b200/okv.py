@@ -558,7 +558,8 @@ def qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps: f
             raise ValueError(f"{name} must be a CUDA tensor on one device with q")
         if len(shape) != 3 or shape[2] != HEAD_DIM or st[2] != 1 or shape[0] != tokens:
             raise ValueError(f"{name} must be [T][heads][{HEAD_DIM}] with contiguous rows, got {tuple(shape)}")
-        return shape, st
+        # the stride of a dimension of one is never used, whatever it says
+        return shape, (st[0] if tokens > 1 else 0, st[1] if shape[1] > 1 else 0)
 
     def result(t, shape, name):
         if t is None:
@@ -580,7 +581,7 @@ def qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps: f
     (qs, qst), (ks, kst) = view(q, "q"), view(k, "k")
     q_out, k_out = result(q_out, qs, "q_out"), result(k_out, ks, "k_out")
     if v is not None:
-        vs, (vt, vh, _) = view(v, "v")
+        vs, (vt, vh) = view(v, "v")
         if vs[1] != ks[1]:
             raise ValueError("k and v must have the same number of heads")
         v_out = result(v_out, vs, "v_out")

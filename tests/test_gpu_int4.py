@@ -448,3 +448,55 @@ def test_chunked_prefill_skips_bad_blocks_and_takes_large_scales(group):
     table[0, 5] = -1
     got = okv.prefill_attention(gc, q, 0, 600, _t(table)).cpu().numpy()
     assert np.isfinite(got).all() and gc.device_status() == okv.DEV_BAD_BLOCK
+
+
+@pytest.mark.parametrize("group", GROUPS)
+@pytest.mark.parametrize("length,tokens,lost", [(600, 40, 29), (598, 150, 29), (597, 5, 3), (600, 600, 29)])
+@pytest.mark.parametrize("bf16", [False, True])
+def test_chunked_prefill_with_a_lost_block_reads_the_rest(group, length, tokens, lost, bf16):
+    """A block id outside the pool: its code positions are skipped, window positions in the same block are not
+    (block 29 holds positions 464 .. 479, the window of 600 tokens starts at 472)."""
+    okv = _okv()
+    hq, hkv = 8, 2
+    gc, oc, lay, _ = fill(35, hq, hkv, [length], group)
+    q, qn = queries(35, tokens, hq, hkv)
+    table = lay.table.copy()
+    table[0, lost] = lay.num_blocks + 1
+    out = torch.empty(tokens, hq, 128, dtype=torch.bfloat16 if bf16 else torch.float32, device="cuda")
+    okv.prefill_attention(gc, q, 0, length, _t(table), out=out)
+    assert gc.device_status() == okv.DEV_BAD_BLOCK
+    gone = np.arange(16 * lost, min(16 * lost + 16, length - 128))
+    want = np.zeros((tokens, hq, 128))
+    for h in range(hkv):
+        keys, vals = (oc.values(0, kind, h, length) for kind in (0, 1))
+        for t in range(tokens):
+            seen = np.setdiff1d(np.arange(length - tokens + t + 1), gone)
+            if not len(seen):
+                continue
+            for j in range(h * hq // hkv, (h + 1) * hq // hkv):
+                x = keys[seen] @ (qn[t, j].astype(np.float64) @ oc.r[0][h]) / math.sqrt(128)
+                w = np.exp(x - x.max())
+                want[t, j] = (w / w.sum()) @ vals[seen] @ oc.r[1][h].T
+    check_rows(out.float().cpu().numpy(), want, TOL + (2.0 ** -8 if bf16 else 0))
+
+
+@pytest.mark.parametrize("group", [128, 32])
+def test_chunked_prefill_rows_keep_apart(group):
+    """An infinite query row leaves the other rows alone; values at the top of fp16 saturate and stay finite."""
+    okv = _okv()
+
+    def put(kind, b, z):
+        if kind == 1:
+            z[::7] *= 3e4
+    gc, oc, lay, _ = fill(36, 8, 2, [500], group, extra=put)
+    q, qn = queries(36, 90, 8, 2)
+    out = torch.empty(90, 8, 128, dtype=torch.bfloat16, device="cuda")
+    okv.prefill_attention(gc, q, 0, 500, _t(lay.table), out=out)
+    assert torch.isfinite(out).all() and gc.device_status() == 0
+    bad = q.clone()
+    bad[33, 5, 7] = float("inf")
+    got = torch.empty_like(out)
+    okv.prefill_attention(gc, bad, 0, 500, _t(lay.table), out=got)
+    keep = torch.ones(90, 8, dtype=torch.bool, device="cuda")
+    keep[33, 5] = False
+    assert torch.equal(got[keep], out[keep])

@@ -144,6 +144,24 @@ def test_head_major_views_and_extreme_rows():
     assert torch.isfinite(out[keep]).all() and not torch.isfinite(out[~keep]).any()
 
 
+def test_one_token_and_one_head_at_any_stride():
+    okv = _okv()
+    g = torch.Generator(device="cuda").manual_seed(4)
+    x = torch.randn(2000, generator=g, device="cuda")
+    q = x.as_strided((1, 4, D), (3, 136, 1), 0)           # one token: its stride is never used
+    k = x.as_strided((1, 1, D), (5, 7, 1), 1000)
+    pos, f = torch.tensor([77], dtype=torch.int32, device="cuda"), freqs(64)
+    got = okv.qk_norm_rope(q, k, pos, f)
+    for y, t in zip(got, (q, k)):
+        close(y, *formula(t, None, pos, f, 1e-6, False, True, 1.0))
+    q = torch.randn(D, generator=g, device="cuda").expand(6, 3, D)  # one row broadcast over tokens and heads
+    pos = torch.arange(6, dtype=torch.int32, device="cuda")
+    y, _ = okv.qk_norm_rope(q, q, pos, f)
+    close(y, *formula(q, None, pos, f, 1e-6, False, True, 1.0))
+    with pytest.raises(ValueError, match="inv_freq"):
+        okv.qk_norm_rope(q, q, pos, None)
+
+
 def test_streams_and_graph():
     okv = _okv()
     qkv, pos, (wq, wk) = inputs(11, 200, 32, 8, torch.bfloat16)
