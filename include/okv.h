@@ -394,7 +394,7 @@ okv_status okv_dequantize(const okv_cache_desc* desc, int32_t B, const int32_t* 
  * step that feeds itself); any other overlap is undefined.
  *   workspace: device, okv_plan_workspace_bytes(num_requests) bytes (about 8
  *   per request), 4-byte aligned; read only by the larger form of the call
- *   (more than 2048 requests or 8192 rows), but a caller passes it always.
+ *   (more than 4096 requests or token rows), but a caller passes it always.
  * One launch for small steps, two else.  Errors: INVALID_ARG (NULL, negative
  * or too large sizes, misaligned arrays, workspace too small), UNSUPPORTED
  * (num_seq_slots above OKV_PLAN_MAX_SLOTS).

@@ -245,9 +245,14 @@ __global__ void __launch_bounds__(kPlFillThreads) plan_fill_kernel(PlanArgs a) {
 }
 
 // One launch up to this many requests and token rows, else the scan and a
-// fill over the whole GPU.
-constexpr int kPlOneCtaRequests = 2048;
-constexpr int kPlOneCtaRows = 8192;
+// fill over the whole GPU.  Measured in a graph, one launch against two:
+// 256 requests with 256 rows 3.6 and 6.4 us, 8 with 4096 rows 5.5 and 5.7, 256
+// with 4096 rows 6.6 and 6.5, 4096 with 4096 rows 13.0 and 14.3; but 8 with
+// 8192 rows 7.5 and 5.8, 256 with 8192 rows 9.7 and 6.8, 8 with 32768 rows
+// 19.6 and 5.8.  So rows decide; more requests than this would not fit the
+// shared memory beside the largest slot bitmap.
+constexpr int kPlOneCtaRequests = 4096;
+constexpr int kPlOneCtaRows = 4096;
 
 }  // namespace
 }  // namespace okv

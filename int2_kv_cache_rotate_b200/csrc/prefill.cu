@@ -1060,10 +1060,11 @@ __global__ void __launch_bounds__(kUpThreads, 1) prefill_umma_kernel(PrefillArgs
 // 3. o = (o' / l) R_V^T (see 1. for the tiling): un-permute, 1 / l and the
 // butterfly per row in registers, the row to shared memory, then o = x U_V^T
 // with U_V^T permuted: ut[i][4 l + j] = U_V[l + 32 j][i].
-// kSplit: o', l and the running maximum of a.splits key ranges per row are
-// merged first (ranges with l = 0 hold nothing and are not read).
+// kSplit: the rows come from the 4-bit kernel, whose tiles may be cut (P4Split):
+// then o', l and the running maximum of a tile's pieces are merged first (pieces
+// with l = 0 hold nothing and are not read).
 template <bool kSplit, int RW>
-__global__ void __launch_bounds__(256) prefill_unrotate_kernel(PrefillArgs a) {
+__global__ void __launch_bounds__(256) prefill_unrotate_kernel(const __grid_constant__ PrefillArgs a, const __grid_constant__ P4Split sp) {
   constexpr int kRtRows = rt_rows(RW);
   extern __shared__ __align__(16) float rt_[];
   float* ut = rt_;
@@ -1102,14 +1103,25 @@ __global__ void __launch_bounds__(256) prefill_unrotate_kernel(PrefillArgs a) {
   const float* src[RW];
 #pragma unroll
   for (int k = 0; k < RW; ++k) src[k] = a.obuf + (size_t)rt_row(a, hk, min(r0 + RW * warp + k, nrows - 1)) * kOStride;
+  int j0 = 0, pieces = 1;  // the tile's first range, and how many hold a piece of it
   if constexpr (kSplit) {
-    // lane s holds (l, maximum) of range s (at most 32 ranges), then its weight 2^(m_s - m)
-    const size_t next = (size_t)a.T * a.hq * kOStride;
+    static_assert(kP4Rows % rt_rows(RW) == 0, "a CTA's rows are in one tile");
+    j0 = sp.ranges_of(hk * sp.tiles + r0 / kP4Rows, pieces);
+  }
+  if (kSplit && pieces > 1) {
+    // lane s holds (l, maximum) of piece s (at most 32), then its weight 2^(m_s - m)
+    const int t0 = r0 / kP4Rows * kP4Rows;
+    const float* first = sp.piece(j0, 1);
+    const float* others = sp.piece(j0, 0);
+    const size_t next = (size_t)2 * sp.prow * kOStride;
+    auto piece_row = [&](int s, int k) {
+      return (s == 0 ? first : others + s * next) + (size_t)(min(r0 + RW * warp + k, nrows - 1) - t0) * kOStride;
+    };
     float w[RW];
 #pragma unroll
     for (int k = 0; k < RW; ++k) {
       const float2 lm =
-          lane < a.splits ? *reinterpret_cast<const float2*>(src[k] + lane * next + 128) : make_float2(0.f, 0.f);
+          lane < pieces ? *reinterpret_cast<const float2*>(piece_row(lane, k) + 128) : make_float2(0.f, 0.f);
       lr[k] = lm.x;
       w[k] = lm.y;
       o4[k] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -1120,15 +1132,15 @@ __global__ void __launch_bounds__(256) prefill_unrotate_kernel(PrefillArgs a) {
       w[k] = lr[k] > 0.f ? exp2f(w[k] - top) : 0.f;
       lr[k] = warp_sum(w[k] * lr[k]);
     }
-    // range by range, the warp's rows' loads in flight together (a row at
-    // a time, 18 ranges took 47 us)
-    for (int s = 0; s < a.splits; ++s) {
+    // piece by piece, the warp's rows' loads in flight together (a row at
+    // a time, 18 pieces took 47 us)
+    for (int s = 0; s < pieces; ++s) {
       float4 x[RW];
       float ws[RW];
 #pragma unroll
       for (int k = 0; k < RW; ++k) {
         ws[k] = __shfl_sync(0xffffffffu, w[k], s);
-        x[k] = ws[k] != 0.f ? *reinterpret_cast<const float4*>(src[k] + s * next + 4 * r) : make_float4(0.f, 0.f, 0.f, 0.f);
+        x[k] = ws[k] != 0.f ? *reinterpret_cast<const float4*>(piece_row(s, k) + 4 * r) : make_float4(0.f, 0.f, 0.f, 0.f);
       }
 #pragma unroll
       for (int k = 0; k < RW; ++k)
@@ -1181,15 +1193,51 @@ __global__ void __launch_bounds__(256) prefill_unrotate_kernel(PrefillArgs a) {
 
 }  // namespace
 
-// Key ranges per row of the 4-bit kernel: as many as fill the GPU when the
-// chunk's row tiles do not (one CTA per SM), at most 32 (a warp's lanes in the
-// merge).  It depends on T alone, so that the workspace does.
-static int prefill_ranges(const okv_cache_desc* d, int T) {
-  if (code_bits(d) != 4 || T == 0) return 1;
-  const int sms = device_sm_count() > 0 ? device_sm_count() : 148;
-  const long long tiles = ((long long)T * (d->num_q_heads / d->num_kv_heads) + kP4Rows - 1) / kP4Rows;
-  const long long ctas = tiles * d->num_kv_heads;
-  return (int)std::max(1ll, std::min(32ll, sms / ctas));
+// The most ranges of the 4-bit kernel's work: one CTA per SM.
+static int prefill_most_ranges() { return std::min(device_sm_count() > 0 ? device_sm_count() : 148, kP4MostCtas); }
+
+static size_t prefill_piece_rows(const okv_cache_desc* d, int T) {
+  return (size_t)std::min<long long>(kP4Rows, (long long)T * (d->num_q_heads / d->num_kv_heads));
+}
+
+// The cut of the 4-bit kernel's work.  One range per SM, where that leaves about
+// two chunks each (or a whole tile), and no tile more than kP4MostPieces pieces.
+// A tile weighs its keys times g, which has closed sums.  1024 tokens over 32K
+// keys (32/8 heads) are 128 tiles, so 128 of 148 SMs with a CTA per tile.
+static P4Split prefill_split(const PrefillArgs& a, int piece_rows, float* part) {
+  P4Split sp;
+  sp.tiles = (int)(((long long)a.T * a.g + kP4Rows - 1) / kP4Rows);
+  sp.prow = piece_rows;
+  sp.part = part;
+  const long long old = (long long)a.first * a.g;
+  auto before = [&](long long x) { return x * (old + kP4Rows / 2 * (x + 1)); };  // tiles 0 .. x - 1
+  auto weight = [&](long long x) { return old + kP4Rows * (x + 1); };
+  const long long head = before(sp.tiles), total = head * a.hkv;
+  const long long most = (kP4MostPieces - 2) * (total / weight(sp.tiles - 1));
+  const int n = (int)std::min(std::min((long long)prefill_most_ranges(), most),
+                              std::max((long long)sp.tiles * a.hkv, total / (2ll * kP4Keys * a.g)));
+  sp.start[0] = make_int2(0, 0);
+  int k = 0;
+  for (int j = 1; j < n; ++j) {
+    const long long u = total / n * j + total % n * j / n, hk = u / head, v = u - hk * head;
+    int lo = 0, hi = sp.tiles - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (before(mid) <= v) lo = mid;
+      else hi = mid - 1;
+    }
+    const int chunks = prefill_last_pos(a, lo) / kP4Keys + 1, snap = chunks >= 16 ? 1 : 0;
+    const long long w = weight(lo);
+    int2 s = make_int2((int)hk * sp.tiles + lo, (int)(((v - before(lo)) * chunks + w / 2) / w));
+    if (s.y <= snap) s.y = 0;  // not worth a piece of its own
+    else if (s.y >= chunks - snap) s = make_int2(s.x + 1, 0);
+    const int2 last = sp.start[k];
+    if (s.x > last.x || (s.x == last.x && s.y > last.y)) sp.start[++k] = s;
+  }
+  if (sp.start[k].x == sp.tiles * a.hkv) --k;
+  sp.ctas = k + 1;
+  sp.start[k + 1] = make_int2(sp.tiles * a.hkv, 0);
+  return sp;
 }
 
 size_t prefill_workspace_bytes(const okv_cache_desc* d, int T) {
@@ -1198,7 +1246,8 @@ size_t prefill_workspace_bytes(const okv_cache_desc* d, int T) {
   off += (rows * kD * sizeof(__half) + 255) / 256 * 256;  // qhi
   off += (rows * kD * sizeof(__half) + 255) / 256 * 256;  // qlo
   off += (rows * kQaux * sizeof(float) + 255) / 256 * 256;
-  off += ((size_t)prefill_ranges(d, T) * rows * kOStride * sizeof(float) + 255) / 256 * 256;
+  off += (rows * kOStride * sizeof(float) + 255) / 256 * 256;
+  if (code_bits(d) == 4) off += 2 * prefill_most_ranges() * prefill_piece_rows(d, T) * kOStride * sizeof(float);
   return off;
 }
 
@@ -1223,6 +1272,7 @@ okv_status launch_prefill(const okv_cache_desc* d, const void* q, int T, int slo
   a.qaux = (float*)(w + off);
   off += (rows * kQaux * sizeof(float) + 255) / 256 * 256;
   a.obuf = (float*)(w + off);
+  off += (rows * kOStride * sizeof(float) + 255) / 256 * 256;
   a.out = out;
   a.T = T;
   a.hq = d->num_q_heads;
@@ -1251,11 +1301,10 @@ okv_status launch_prefill(const okv_cache_desc* d, const void* q, int T, int slo
   qrot<<<rt_grid, 256, rt_bytes, s>>>(a);
   okv_status st = check_launch("prefill query rotation");
   if (st != OKV_OK) return st;
-  a.splits = 1;
+  P4Split sp{};
   if (int4_bf16) {
-    // no more ranges than leave two chunks of 128 keys each
-    a.splits = std::max(1, std::min(prefill_ranges(d, T), (context_len + 255) / 256));
-    st = launch_prefill_int4_bf16(a, s);
+    sp = prefill_split(a, (int)prefill_piece_rows(d, T), (float*)(w + off));
+    st = launch_prefill_int4_bf16(a, sp, s);
   } else {
     const dim3 grid((unsigned)((T * a.g + kPfRows - 1) / kPfRows), (unsigned)a.hkv);
     using Kernel = void (*)(PrefillArgs);
@@ -1274,11 +1323,11 @@ okv_status launch_prefill(const okv_cache_desc* d, const void* q, int T, int slo
   // CTAs run: it stages U_V, then waits for the attention's outputs.  Starting
   // the attention early behind the query rotation in the same way measured
   // slower with 64-channel groups (3.31 against 3.10 ms) and is not done.
-  const auto unrotate = a.splits > 1 ? (small ? prefill_unrotate_kernel<true, 2> : prefill_unrotate_kernel<true, 8>)
-                                     : (small ? prefill_unrotate_kernel<false, 2> : prefill_unrotate_kernel<false, 8>);
-  e0 = set_smem_limit_once((const void*)unrotate, (int)rt_bytes, ur_attr[a.splits > 1][small]);
+  const auto unrotate = int4_bf16 ? (small ? prefill_unrotate_kernel<true, 2> : prefill_unrotate_kernel<true, 8>)
+                                  : (small ? prefill_unrotate_kernel<false, 2> : prefill_unrotate_kernel<false, 8>);
+  e0 = set_smem_limit_once((const void*)unrotate, (int)rt_bytes, ur_attr[int4_bf16][small]);
   if (e0 != cudaSuccess) return fail(OKV_ERR_CUDA, "prefill rotation smem attribute: %s", cudaGetErrorString(e0));
-  const cudaError_t e3 = launch_pdl(unrotate, rt_grid, dim3(256), rt_bytes, s, true, a);
+  const cudaError_t e3 = launch_pdl(unrotate, rt_grid, dim3(256), rt_bytes, s, true, a, sp);
   if (e3 != cudaSuccess) return fail(OKV_ERR_CUDA, "prefill un-rotation launch: %s", cudaGetErrorString(e3));
   return check_launch("prefill un-rotation");
 }

@@ -11,8 +11,8 @@
 // per-key factor and one kernel body serves every group size.  Values past
 // fp16's +-65504 saturate, like the cache's fp16 rows.
 //
-// A CTA takes 256 query rows (two tiles of 128, the MMA's M) of one KV head
-// and one range of the key positions, and streams it in chunks of 128 keys:
+// A CTA takes its range of the work (P4Split): piece by piece, 256 query rows
+// (two tiles of 128, the MMA's M) of one KV head against a run of 128-key chunks:
 //   warps 0-3, 4-7  softmax of tile 0 and 1: a thread owns a row (TMEM lane);
 //   warps 8-11      keys into shared memory, [token][channel] fp16, and values,
 //                   [channel][token] fp16, both K-major (13 warps leave 128
@@ -35,7 +35,11 @@
 // 6 3 7 within eight, and keys in the order 0 2 1 3 within four, in the score
 // columns and in the value tile alike.
 // Bound: 128 keys x 256 rows cost 32 MMAs of 64 cycles and 32768 exponentials
-// at 16 a cycle, 2048 cycles each.
+// at 16 a cycle, 2048 cycles each; a chunk takes 5250 (1024 tokens over 32K keys,
+// 32/8 heads: 640 us, 860 TFLOP/s), the exponential unit and the tensor pipe
+// 39 % busy, issue slots 45 %: what is left is the latency of each tile's chain
+// of scores, softmax and value MMA.  One range of work per SM against one tile
+// per CTA (128 of them): 762 against 873 us a call.
 #include <type_traits>
 
 #include "okv_common.cuh"
@@ -46,7 +50,6 @@
 namespace okv {
 namespace {
 
-constexpr int kP4Keys = 128;                  // key positions per chunk
 constexpr int kP4Threads = 32 * 13;
 constexpr uint32_t kP4Tile = 32768;           // a 128 x 128 fp16 tile: two K-blocks of 128 rows x 128 B
 constexpr uint32_t kP4OffQ = 0;               // Q_0, Q_1
@@ -54,7 +57,7 @@ constexpr uint32_t kP4OffK = 2 * kP4Tile;     // two stages
 constexpr uint32_t kP4OffV = 4 * kP4Tile;     // two stages
 constexpr uint32_t kP4OffMisc = 6 * kP4Tile;
 struct P4Misc {
-  uint64_t k_full[2], k_free[2], v_full[2], v_free[2], s_full[2], p_full[2], pv_done[2];
+  uint64_t q_full[2], k_full[2], k_free[2], v_full[2], v_free[2], s_full[2], p_full[2], pv_done[2];
   int bad[4][4];               // per chunk mod 4, key warp: a block id was out of range
   int kval[4][kP4Keys];        // then: 1 where the token was staged
   uint32_t tmem_slot;
@@ -93,7 +96,8 @@ __device__ __forceinline__ uint32_t sat_h2(uint32_t x) {  // infinities to the l
 }
 
 template <int NG>
-__global__ void __launch_bounds__(kP4Threads, 1) prefill_int4_kernel(PrefillArgs a) {
+__global__ void __launch_bounds__(kP4Threads, 1)
+    prefill_int4_kernel(const __grid_constant__ PrefillArgs a, const __grid_constant__ P4Split sp) {
   extern __shared__ unsigned char p4_raw[];
   const uint32_t raw_u32 = smem_u32(p4_raw);
   const uint32_t base = (raw_u32 + 1023u) & ~1023u;  // swizzle atoms need 1024-byte alignment
@@ -101,19 +105,13 @@ __global__ void __launch_bounds__(kP4Threads, 1) prefill_int4_kernel(PrefillArgs
   P4Misc& ms = *reinterpret_cast<P4Misc*>(gb + kP4OffMisc);
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int hk = blockIdx.y;
   const int nrows = a.T * a.g;
-  const int row0 = blockIdx.x * kP4Rows;
-  const int nt = row0 + 128 < nrows ? 2 : 1;  // tiles with any row
-  const int pmax = a.first + (min(nrows, row0 + kP4Rows) - 1) / a.g;  // last position any row of this CTA sees
-  const int nch_all = pmax / kP4Keys + 1;
-  const int c0 = (int)((long long)blockIdx.z * nch_all / a.splits);
-  const int n = (int)((long long)(blockIdx.z + 1) * nch_all / a.splits) - c0;  // chunks c0 .. c0 + n - 1
   const int32_t* table = a.block_table + (size_t)a.slot * a.mbps;
   grid_dep_launch();  // the un-rotation may start staging U_V
 
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
+      mbar_init(&ms.q_full[i], 128);
       mbar_init(&ms.k_full[i], 128);
       mbar_init(&ms.k_free[i], 1);
       mbar_init(&ms.v_full[i], 128);
@@ -126,52 +124,34 @@ __global__ void __launch_bounds__(kP4Threads, 1) prefill_int4_kernel(PrefillArgs
   }
   if (warp == 12) um_alloc(&ms.tmem_slot, 512);
 
-  // the row of a softmax thread, and its q~ into the Q tile
+  // this CTA's pieces, the same for every role
+  struct Piece {
+    int hk, x;  // KV head, tile of the head
+    int c0, n;  // chunks c0 .. c0 + n - 1
+    int nt;     // 128-row tiles with any row
+    int slot;   // where the rows go: -1 obuf (the whole tile), else the slot of `part`
+  };
+  const int2 u_begin = sp.start[blockIdx.x], u_end = sp.start[blockIdx.x + 1];
+  auto more = [&](int2 u) { return u.x < u_end.x || u.y < u_end.y; };
+  auto next_piece = [&](int2 u, Piece& pc) -> int2 {
+    pc.hk = u.x / sp.tiles;
+    pc.x = u.x - pc.hk * sp.tiles;
+    pc.c0 = u.y;
+    const bool cut = u.x == u_end.x;
+    pc.n = (cut ? u_end.y : prefill_last_pos(a, pc.x) / kP4Keys + 1) - pc.c0;
+    pc.nt = pc.x * kP4Rows + 128 < nrows ? 2 : 1;
+    pc.slot = pc.c0 > 0 ? 0 : cut ? 1 : -1;
+    return cut ? u_end : make_int2(u.x + 1, 0);
+  };
+
   const int tile = (warp >> 2) & 1, quarter = warp & 3;
-  const int trow = 32 * quarter + lane;  // row in the tile (TMEM lane)
-  int rrow = 0, rpos = 0;
-  bool rok = false;
-  float sc = 0.f;  // score scale in log2 units: 2^e log2(e) / sqrt(d)
-  if (warp < 8) {
-    const int r = row0 + 128 * tile + trow;
-    rok = r < nrows;
-    const int rr = rok ? r : nrows - 1;
-    const int rtok = rr / a.g;
-    rrow = rtok * a.hq + hk * a.g + rr % a.g;
-    rpos = a.first + rtok;
-    const uint4* src = reinterpret_cast<const uint4*>(a.qhi + (size_t)rrow * kD);
-    unsigned char* dst = gb + kP4OffQ + (uint32_t)tile * kP4Tile;
-#pragma unroll
-    for (int j = 0; j < 16; ++j)
-      *reinterpret_cast<uint4*>(dst + (j >> 3) * 16384 + um_swz((uint32_t)trow, (uint32_t)(j & 7) * 16u)) = src[j];
-    sc = a.qaux[(size_t)rrow * kQaux + 4] * (kInvSqrtD * kLog2e);
-    um_fence_proxy_async();
-  }
+  const int trow = 32 * quarter + lane;  // row in the tile (TMEM lane) of a softmax thread
   um_fence_before();
   __syncthreads();
   um_fence_after();
   const uint32_t tmem = ms.tmem_slot;
   const uint32_t tS = tmem + 128u * (uint32_t)tile, tO = tmem + 256u + 128u * (uint32_t)tile;
 
-  // fp16 row (sink or window ring) of position p
-  auto fp16_row = [&](int p, int kind) -> const __half* {
-    const bool sink = p < a.nsink;
-    const size_t rows = sink ? (size_t)a.nsink : (size_t)kWin;
-    const size_t row = sink ? (size_t)p : (size_t)(p % kWin);
-    return (sink ? a.sink : a.ring) + ((((size_t)a.slot * a.hkv + hk) * 2 + kind) * rows + row) * kD;
-  };
-  // where position p is read from: 0 nowhere, 1 codes (block blk), 2 an fp16 row
-  auto source = [&](int p, int blk) -> int {
-    if (p > pmax || p >= a.L) return 0;
-    if (p < a.nsink || p >= a.L - kWin) return 2;
-    if (blk < 0 || blk >= a.num_blocks) {
-      raise_flag(a.status, OKV_DEV_BAD_BLOCK);
-      return 0;
-    }
-    return 1;
-  };
-  auto block_of = [&](int p) -> int { return p <= pmax && p < a.L ? __ldg(table + (p >> 4)) : -1; };
-  auto head_of = [&](int blk) { return a.pages + ((size_t)blk * a.hkv + hk) * a.bhb; };
   // key order within a quad: token t sits at row swap_mid(t), row r holds token swap_mid(r)
   auto swap_mid = [](int t) { return (t & ~3) | ((t & 1) << 1) | ((t & 2) >> 1); };
   constexpr int kSm = 2048;  // (scale, min) pairs of the keys; the values' follow 64 NG bytes on
@@ -179,120 +159,166 @@ __global__ void __launch_bounds__(kP4Threads, 1) prefill_int4_kernel(PrefillArgs
   if (warp < 8) {
     // ------------------------------------------------------------ softmax
     const uint32_t lb = (uint32_t)(32 * quarter) << 16;
-    float m_use = -INFINITY;
-    float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};  // partial sums of the weights
-    const float2 sc2 = make_float2(sc, sc);
-    bool alive = tile < nt;
-    for (int i = 0; i < n && alive; ++i) {
-      const uint32_t ph = (uint32_t)i & 1u;
-      alive = __all_sync(0xffffffffu, mbar_wait_bounded(&ms.s_full[tile], ph));
-      if (!alive) break;
-      um_fence_after();
-      const int c = c0 + i;
-      const int lim = min(rpos + 1, a.L) - kP4Keys * c;  // columns below it are visible
-      const int* bd = ms.bad[c & 3];
-      const bool bad = (bd[0] | bd[1] | bd[2] | bd[3]) != 0;
-      // A batch of 32 columns at a time, rolled up: the loops of the three roles
-      // share the instruction cache, and the smallest body was the fastest (one
-      // batch per turn 791 us a call, two with the second's loads ahead 806, all
-      // four unrolled 836; with the causal mask's selects inside, 860).
-      auto weights = [&](auto masked) {
+    bool alive = true;
+    int done = 0, seen = 0;  // chunks of the pieces before: staged, and those with this tile
+    Piece pc;
 #pragma unroll 1
-        for (int b = 0; b < 4; ++b) {
-          float x[32];
-          um_ld32(tS + lb + 32u * b, x);
-          um_wait_ld();
-          if constexpr (decltype(masked)::value) {
-            const int* kv = &ms.kval[c & 3][32 * b];
+    for (int2 u = u_begin; more(u); done += pc.n) {
+      u = next_piece(u, pc);
+      if (tile >= pc.nt) continue;
+      // the thread's row, and its q~ into the Q tile (the MMAs that read the last one are done: pv_done)
+      const int r = pc.x * kP4Rows + 128 * tile + trow;
+      const bool rok = r < nrows;
+      const int rr = rok ? r : nrows - 1;
+      const int rtok = rr / a.g, rpos = a.first + rtok;
+      const size_t rrow = (size_t)rtok * a.hq + pc.hk * a.g + rr % a.g;
+      {
+        const uint4* src = reinterpret_cast<const uint4*>(a.qhi + rrow * kD);
+        unsigned char* dst = gb + kP4OffQ + (uint32_t)tile * kP4Tile;
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              x[j] = (32 * b + swap_mid(j) < lim && (!bad || kv[j] != 0)) ? x[j] : -INFINITY;
-          }
-          float mx[2] = {fmaxf(x[0], x[1]), fmaxf(x[2], x[3])};
-#pragma unroll
-          for (int j = 4; j < 32; j += 4) {
-            mx[0] = max3(mx[0], x[j], x[j + 1]);
-            mx[1] = max3(mx[1], x[j + 2], x[j + 3]);
-          }
-          const float bm = fmaxf(mx[0], mx[1]) * sc;
-          const bool need = bm > m_use + kP4Slack;
-          if (__any_sync(0xffffffffu, need)) {
-            // O_t holds every earlier chunk (S_t of this one was issued after its MMAs were done)
-            const float alpha = need ? p4_ex2(m_use - bm) : 1.f;  // 0 while the row has seen nothing
-            if (i > 0) {
+        for (int j = 0; j < 16; ++j)
+          *reinterpret_cast<uint4*>(dst + (j >> 3) * 16384 + um_swz((uint32_t)trow, (uint32_t)(j & 7) * 16u)) = src[j];
+        um_fence_proxy_async();
+        mbar_arrive(&ms.q_full[tile]);
+      }
+      const float sc = a.qaux[rrow * kQaux + 4] * (kInvSqrtD * kLog2e);  // score scale, log2 units: 2^e log2(e) / sqrt(d)
+      const float2 sc2 = make_float2(sc, sc);
+      float m_use = -INFINITY;
+      float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};  // partial sums of the weights
+      for (int i = 0; i < pc.n && alive; ++i) {
+        const uint32_t ph = (uint32_t)(seen + i) & 1u;
+        alive = __all_sync(0xffffffffu, mbar_wait_bounded(&ms.s_full[tile], ph));
+        if (!alive) break;
+        um_fence_after();
+        const int kb = (done + i) & 3;
+        const int lim = min(rpos + 1, a.L) - kP4Keys * (pc.c0 + i);  // columns below it are visible
+        const int* bd = ms.bad[kb];
+        const bool bad = (bd[0] | bd[1] | bd[2] | bd[3]) != 0;
+        // A batch of 32 columns at a time, rolled up: the loops of the three roles
+        // share the instruction cache, and the smallest body was the fastest (one
+        // batch per turn 791 us a call, two with the second's loads ahead 806, all
+        // four unrolled 836; with the causal mask's selects inside, 860).
+        auto weights = [&](auto masked) {
 #pragma unroll 1
-              for (int q = 0; q < 8; ++q) {
-                uint32_t o[16];
-                um_ld16(tO + lb + 16u * q, o);
+          for (int b = 0; b < 4; ++b) {
+            float x[32];
+            um_ld32(tS + lb + 32u * b, x);
+            um_wait_ld();
+            if constexpr (decltype(masked)::value) {
+              const int* kv = &ms.kval[kb][32 * b];
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                x[j] = (32 * b + swap_mid(j) < lim && (!bad || kv[j] != 0)) ? x[j] : -INFINITY;
+            }
+            float mx[2] = {fmaxf(x[0], x[1]), fmaxf(x[2], x[3])};
+#pragma unroll
+            for (int j = 4; j < 32; j += 4) {
+              mx[0] = max3(mx[0], x[j], x[j + 1]);
+              mx[1] = max3(mx[1], x[j + 2], x[j + 3]);
+            }
+            const float bm = fmaxf(mx[0], mx[1]) * sc;
+            const bool need = bm > m_use + kP4Slack;
+            if (__any_sync(0xffffffffu, need)) {
+              // O_t holds every earlier chunk (S_t of this one was issued after its MMAs were done)
+              const float alpha = need ? p4_ex2(m_use - bm) : 1.f;  // 0 while the row has seen nothing
+              if (i > 0) {
+#pragma unroll 1
+                for (int q = 0; q < 8; ++q) {
+                  uint32_t o[16];
+                  um_ld16(tO + lb + 16u * q, o);
+                  um_wait_ld();
+#pragma unroll
+                  for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
+                  um_st16(tO + lb + 16u * q, o);
+                }
+              }
+#pragma unroll 1
+              for (int q = 0; q < b; ++q) {  // weights of this chunk's batches before: columns 16 q ..
+                uint32_t u[16];
+                um_ld16(tS + lb + 16u * q, u);
                 um_wait_ld();
 #pragma unroll
-                for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
-                um_st16(tO + lb + 16u * q, o);
+                for (int j = 0; j < 16; ++j) {
+                  const float2 f = __half22float2(bits_h2(u[j]));
+                  u[j] = h2_bits(__floats2half2_rn(f.x * alpha, f.y * alpha));
+                }
+                um_st16(tS + lb + 16u * q, u);
               }
+              um_wait_st();
+              ls[0] = __fmul2_rn(ls[0], make_float2(alpha, alpha));
+              ls[1] = __fmul2_rn(ls[1], make_float2(alpha, alpha));
+              if (need) m_use = bm;
             }
-#pragma unroll 1
-            for (int q = 0; q < b; ++q) {  // weights of this chunk's batches before: columns 16 q ..
-              uint32_t u[16];
-              um_ld16(tS + lb + 16u * q, u);
-              um_wait_ld();
+            const float nm = kP4Offset - (m_use == -INFINITY ? 0.f : m_use);
+            const float2 nm2 = make_float2(nm, nm);
+            uint32_t w[16];
 #pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                const float2 f = __half22float2(bits_h2(u[j]));
-                u[j] = h2_bits(__floats2half2_rn(f.x * alpha, f.y * alpha));
-              }
-              um_st16(tS + lb + 16u * q, u);
+            for (int j = 0; j < 16; ++j) {
+              const float2 d = __ffma2_rn(make_float2(x[2 * j], x[2 * j + 1]), sc2, nm2);
+              const float2 p = make_float2(p4_ex2(d.x), p4_ex2(d.y));
+              ls[j & 1] = __fadd2_rn(ls[j & 1], p);
+              w[j] = h2_bits(__floats2half2_rn(p.x, p.y));
             }
-            um_wait_st();
-            ls[0] = __fmul2_rn(ls[0], make_float2(alpha, alpha));
-            ls[1] = __fmul2_rn(ls[1], make_float2(alpha, alpha));
-            if (need) m_use = bm;
+            um_st16(tS + lb + 16u * b, w);
           }
-          const float nm = kP4Offset - (m_use == -INFINITY ? 0.f : m_use);
-          const float2 nm2 = make_float2(nm, nm);
-          uint32_t w[16];
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const float2 d = __ffma2_rn(make_float2(x[2 * j], x[2 * j + 1]), sc2, nm2);
-            const float2 p = make_float2(p4_ex2(d.x), p4_ex2(d.y));
-            ls[j & 1] = __fadd2_rn(ls[j & 1], p);
-            w[j] = h2_bits(__floats2half2_rn(p.x, p.y));
-          }
-          um_st16(tS + lb + 16u * b, w);
-        }
-      };
-      // (the whole warp one way: the bodies are warp-collective)
-      if (__builtin_expect(__any_sync(0xffffffffu, lim < kP4Keys || bad), 0)) weights(std::true_type{});
-      else weights(std::false_type{});
-      um_wait_st();
-      um_fence_before();
-      mbar_arrive(&ms.p_full[tile]);
-    }
-    if (n > 0 && alive) {
-      alive = mbar_wait_bounded(&ms.pv_done[tile], (uint32_t)(n - 1) & 1u);
-      alive = __all_sync(0xffffffffu, alive);
-    }
-    if (tile < nt) {
-      float* dst = a.obuf + ((size_t)blockIdx.z * a.T * a.hq + rrow) * kOStride;
-      if (alive && n > 0) {
-        um_fence_after();
-#pragma unroll 1
-        for (int q = 0; q < 4; ++q) {
-          float o[32];
-          um_ld32(tO + lb + 32u * q, o);
-          um_wait_ld();
-          if (rok) {
-#pragma unroll
-            for (int j = 0; j < 32; j += 4)
-              *reinterpret_cast<float4*>(dst + 32 * q + j) = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
-          }
-        }
+        };
+        // (the whole warp one way: the bodies are warp-collective)
+        if (__builtin_expect(__any_sync(0xffffffffu, lim < kP4Keys || bad), 0)) weights(std::true_type{});
+        else weights(std::false_type{});
+        um_wait_st();
+        um_fence_before();
+        mbar_arrive(&ms.p_full[tile]);
       }
-      // a range without keys, or without a visible one, has l = 0 and is skipped by the merge
-      if (rok) *reinterpret_cast<float2*>(dst + 128) = make_float2(alive ? (ls[0].x + ls[0].y) + (ls[1].x + ls[1].y) : 0.f, m_use);
-      if (!alive && lane == 0) raise_flag(a.status, OKV_DEV_TIMEOUT);
+      seen += pc.n;
+      if (alive) {
+        alive = mbar_wait_bounded(&ms.pv_done[tile], (uint32_t)(seen - 1) & 1u);
+        alive = __all_sync(0xffffffffu, alive);
+      }
+      {
+        float* dst = pc.slot < 0 ? a.obuf + rrow * kOStride
+                                 : sp.piece(blockIdx.x, pc.slot) + (size_t)(128 * tile + trow) * kOStride;
+        if (alive) {
+          um_fence_after();
+#pragma unroll 1
+          for (int q = 0; q < 4; ++q) {
+            float o[32];
+            um_ld32(tO + lb + 32u * q, o);
+            um_wait_ld();
+            if (rok) {
+#pragma unroll
+              for (int j = 0; j < 32; j += 4)
+                *reinterpret_cast<float4*>(dst + 32 * q + j) = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+            }
+          }
+        }
+        // a piece without a visible key has l = 0 and is skipped by the merge
+        const float l = alive ? (ls[0].x + ls[0].y) + (ls[1].x + ls[1].y) : 0.f;
+        if (rok) *reinterpret_cast<float2*>(dst + 128) = make_float2(l, m_use);
+      }
     }
+    if (!alive && lane == 0) raise_flag(a.status, OKV_DEV_TIMEOUT);
   } else if (warp < 12) {
     // ------------------------------------------------------------ staging
+    int hk = 0, pmax = 0;
+    // fp16 row (sink or window ring) of position p
+    auto fp16_row = [&](int p, int kind) -> const __half* {
+      const bool sink = p < a.nsink;
+      const size_t rows = sink ? (size_t)a.nsink : (size_t)kWin;
+      const size_t row = sink ? (size_t)p : (size_t)(p % kWin);
+      return (sink ? a.sink : a.ring) + ((((size_t)a.slot * a.hkv + hk) * 2 + kind) * rows + row) * kD;
+    };
+    // where position p is read from: 0 nowhere, 1 codes (block blk), 2 an fp16 row
+    auto source = [&](int p, int blk) -> int {
+      if (p > pmax || p >= a.L) return 0;
+      if (p < a.nsink || p >= a.L - kWin) return 2;
+      if (blk < 0 || blk >= a.num_blocks) {
+        raise_flag(a.status, OKV_DEV_BAD_BLOCK);
+        return 0;
+      }
+      return 1;
+    };
+    auto block_of = [&](int p) -> int { return p <= pmax && p < a.L ? __ldg(table + (p >> 4)) : -1; };
+    auto head_of = [&](int blk) { return a.pages + ((size_t)blk * a.hkv + hk) * a.bhb; };
     // keys: thread = token of the chunk
     const int kt = tid - 256, krow = swap_mid(kt);
     struct FetchedK {
@@ -346,33 +372,38 @@ __global__ void __launch_bounds__(kP4Threads, 1) prefill_int4_kernel(PrefillArgs
       const uint4& q = fv.sm[bb][w >> 2];
       return (w & 3) == 0 ? q.x : (w & 3) == 1 ? q.y : (w & 3) == 2 ? q.z : q.w;
     };
-    int kblk = block_of(kP4Keys * c0 + kt), vblk[2];  // block ids one chunk ahead of the codes
+    int done = 0;  // chunks of the pieces before
+    bool alive = true;
+    Piece pc;
+#pragma unroll 1
+    for (int2 u = u_begin; more(u) && alive; done += pc.n) {
+      u = next_piece(u, pc);
+      hk = pc.hk;
+      pmax = prefill_last_pos(a, pc.x);
+      int kblk = block_of(kP4Keys * pc.c0 + kt), vblk[2];  // block ids one chunk ahead of the codes
 #pragma unroll
-    for (int bb = 0; bb < 2; ++bb) vblk[bb] = block_of(quad_pos(c0, bb));
-    if (n > 0) {
-      fetch_k(c0, kblk);
-      fetch_v(c0, vblk);
-    }
-    kblk = block_of(kP4Keys * (c0 + 1) + kt);
+      for (int bb = 0; bb < 2; ++bb) vblk[bb] = block_of(quad_pos(pc.c0, bb));
+      fetch_k(pc.c0, kblk);
+      fetch_v(pc.c0, vblk);
+      kblk = block_of(kP4Keys * (pc.c0 + 1) + kt);
 #pragma unroll
-    for (int bb = 0; bb < 2; ++bb) vblk[bb] = block_of(quad_pos(c0 + 1, bb));
-    for (int i = 0; i < n; ++i) {
-      const int c = c0 + i, st = i & 1;
-      const uint32_t ph = (uint32_t)((i >> 1) - 1) & 1u;
-      if (i >= 2 && !mbar_wait_bounded(&ms.k_free[st], ph)) {
-        raise_flag(a.status, OKV_DEV_TIMEOUT);
-        break;
-      }
-      {
-        unsigned char* dst = gb + kP4OffK + (uint32_t)st * kP4Tile;
-        if (__builtin_expect(fk.src == 1, 1)) {
-          bool big = false;  // |s c + m| may pass fp16's range
+      for (int bb = 0; bb < 2; ++bb) vblk[bb] = block_of(quad_pos(pc.c0 + 1, bb));
+      for (int i = 0; i < pc.n; ++i) {
+        const int c = pc.c0 + i, at = done + i, st = at & 1;
+        const uint32_t ph = (uint32_t)((at >> 1) - 1) & 1u;
+        if (at >= 2 && !(alive = __all_sync(0xffffffffu, mbar_wait_bounded(&ms.k_free[st], ph)) != 0)) {
+          raise_flag(a.status, OKV_DEV_TIMEOUT);
+          break;
+        }
+        {
+          unsigned char* dst = gb + kP4OffK + (uint32_t)st * kP4Tile;
+          bool easy = fk.src == 1;  // codes, and no |s c + m| past fp16's range
 #pragma unroll
           for (int k = 0; k < NG; ++k) {
             const __half2 sm = bits_h2(fk.sm[k]);
-            big = big || 15.f * __low2float(sm) + fabsf(__high2float(sm)) > 65504.f;
+            easy = easy && 15.f * __low2float(sm) + fabsf(__high2float(sm)) <= 65504.f;
           }
-          auto convert = [&](auto sat) {
+          if (__builtin_expect(easy, 1)) {
 #pragma unroll
             for (int s = 0; s < 4; ++s) {
               const __half2 sm = bits_h2(fk.sm[s * NG / 4]);
@@ -382,56 +413,69 @@ __global__ void __launch_bounds__(kP4Threads, 1) prefill_int4_kernel(PrefillArgs
                 // word s of chunk j: channels 32 s + 8 j .. + 7, low halves even
                 const uint32_t w = s == 0 ? fk.w[j].x : s == 1 ? fk.w[j].y : s == 2 ? fk.w[j].z : fk.w[j].w;
                 const uint32_t y = w >> 8;
-                uint4 o = make_uint4(p4_even(w, s2, m2), p4_odd(w, s2, m2), p4_even(y, s2, m2), p4_odd(y, s2, m2));
-                if constexpr (decltype(sat)::value) o = make_uint4(sat_h2(o.x), sat_h2(o.y), sat_h2(o.z), sat_h2(o.w));
                 *reinterpret_cast<uint4*>(dst + (s >> 1) * 16384 +
-                                          um_swz((uint32_t)krow, (uint32_t)(4 * (s & 1) + j) * 16u)) = o;
+                                          um_swz((uint32_t)krow, (uint32_t)(4 * (s & 1) + j) * 16u)) =
+                    make_uint4(p4_even(w, s2, m2), p4_odd(w, s2, m2), p4_even(y, s2, m2), p4_odd(y, s2, m2));
               }
             }
-          };
-          if (__builtin_expect(big, 0)) convert(std::true_type{});
-          else convert(std::false_type{});
-        } else {
-          const uint4* x = fk.src == 2 ? reinterpret_cast<const uint4*>(fp16_row(kP4Keys * c + kt, 0)) : nullptr;
+          } else if (fk.src != 1) {  // an fp16 row, or a key nobody reads
+            const uint4* row = fk.src == 2 ? reinterpret_cast<const uint4*>(fp16_row(kP4Keys * c + kt, 0)) : nullptr;
+#pragma unroll 1
+            for (int h = 0; h < 16; h += 8) {
+              uint4 y[8];
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const uint4 y = x != nullptr ? x[j] : make_uint4(0, 0, 0, 0);  // into the order 0 4 1 5 2 6 3 7
-            *reinterpret_cast<uint4*>(dst + (j >> 3) * 16384 + um_swz((uint32_t)krow, (uint32_t)(j & 7) * 16u)) =
-                make_uint4(__byte_perm(y.x, y.z, 0x5410u), __byte_perm(y.x, y.z, 0x7632u),
-                           __byte_perm(y.y, y.w, 0x5410u), __byte_perm(y.y, y.w, 0x7632u));
+              for (int j = 0; j < 8; ++j) y[j] = row != nullptr ? row[h + j] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+              for (int j = 0; j < 8; ++j)  // into the order 0 4 1 5 2 6 3 7
+                *reinterpret_cast<uint4*>(dst + h * 2048 + um_swz((uint32_t)krow, (uint32_t)j * 16u)) =
+                    make_uint4(__byte_perm(y[j].x, y[j].z, 0x5410u), __byte_perm(y[j].x, y[j].z, 0x7632u),
+                               __byte_perm(y[j].y, y[j].w, 0x5410u), __byte_perm(y[j].y, y[j].w, 0x7632u));
+            }
+          } else {  // values that saturate, from global memory; rolled up, as what is rare stays out of the instruction cache
+            const int p = kP4Keys * c + kt;
+            const uint8_t* bp = head_of(__ldg(table + (p >> 4)));
+#pragma unroll 1
+            for (int j = 0; j < 16; ++j) {  // channels 8 j .. + 7
+              const uint32_t w = *reinterpret_cast<const uint32_t*>(bp + (p & 15) * 64 + (j & 3) * 16 + (j >> 2) * 4);
+              const __half2 sm = *reinterpret_cast<const __half2*>(bp + kSm + ((p & 15) * NG + (j >> 2) * NG / 4) * 4);
+              const __half2 s2 = __low2half2(sm), m2 = __high2half2(sm);
+              const uint32_t y = w >> 8;
+              *reinterpret_cast<uint4*>(dst + (j >> 3) * 16384 + um_swz((uint32_t)krow, (uint32_t)(j & 7) * 16u)) =
+                  make_uint4(sat_h2(p4_even(w, s2, m2)), sat_h2(p4_odd(w, s2, m2)), sat_h2(p4_even(y, s2, m2)),
+                             sat_h2(p4_odd(y, s2, m2)));
+            }
           }
+          const int p = kP4Keys * c + kt;
+          const bool lost = fk.src == 0 && p <= pmax && p < a.L;  // a visible position without its block
+          ms.kval[at & 3][krow] = !lost;
+          const int any = __any_sync(0xffffffffu, lost);
+          if (lane == 0) ms.bad[at & 3][warp - 8] = any;
         }
-        const int p = kP4Keys * c + kt;
-        const bool lost = fk.src == 0 && p <= pmax && p < a.L;  // a visible position without its block
-        ms.kval[c & 3][krow] = !lost;
-        const int any = __any_sync(0xffffffffu, lost);
-        if (lane == 0) ms.bad[c & 3][warp - 8] = any;
-      }
-      um_fence_proxy_async();
-      mbar_arrive(&ms.k_full[st]);
-      if (i >= 2 && !mbar_wait_bounded(&ms.v_free[st], ph)) {
-        raise_flag(a.status, OKV_DEV_TIMEOUT);
-        break;
-      }
-      unsigned char* dst = gb + kP4OffV + (uint32_t)st * kP4Tile;
-#pragma unroll
-      for (int bb = 0; bb < 2; ++bb) {
-        const int blk16 = 2 * vw + bb;  // block of the chunk
-        unsigned char* vdst = dst + (blk16 >> 2) * 16384;
-        const uint32_t col = (uint32_t)(16 * (blk16 & 3) + 4 * tq) * 2u;
-        auto put = [&](int ch, uint32_t t02, uint32_t t13) {  // the quad's four tokens of channel ch
-          *reinterpret_cast<uint2*>(vdst + um_swz((uint32_t)ch, col)) = make_uint2(t02, t13);
+        um_fence_proxy_async();
+        mbar_arrive(&ms.k_full[st]);
+        if (at >= 2 && !(alive = __all_sync(0xffffffffu, mbar_wait_bounded(&ms.v_free[st], ph)) != 0)) {
+          raise_flag(a.status, OKV_DEV_TIMEOUT);
+          break;
+        }
+        unsigned char* dst = gb + kP4OffV + (uint32_t)st * kP4Tile;
+        // the quad's four tokens of channel ch, of the thread's block bb
+        auto put = [&](int bb, int ch, uint32_t t02, uint32_t t13) {
+          const int blk16 = 2 * vw + bb;  // block of the chunk
+          *reinterpret_cast<uint2*>(dst + (blk16 >> 2) * 16384 +
+                                    um_swz((uint32_t)ch, (uint32_t)(16 * (blk16 & 3) + 4 * tq) * 2u)) = make_uint2(t02, t13);
         };
-        if (__builtin_expect(fv.src[bb] == 1, 1)) {
-          bool big = false;
+        uint32_t rare = 0;  // blocks left to the loop below
+#pragma unroll
+        for (int bb = 0; bb < 2; ++bb) {
+          bool easy = fv.src[bb] == 1;
 #pragma unroll
           for (int k = 0; k < NG; ++k)
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
               const __half2 sm = bits_h2(pair_word(bb, t, k));
-              big = big || 15.f * __low2float(sm) + fabsf(__high2float(sm)) > 65504.f;
+              easy = easy && 15.f * __low2float(sm) + fabsf(__high2float(sm)) <= 65504.f;
             }
-          auto convert = [&](auto sat) {
+          if (__builtin_expect(easy, 1)) {
 #pragma unroll
             for (int k = 0; k < NG; ++k) {
               const uint32_t q0 = pair_word(bb, 0, k), q1 = pair_word(bb, 1, k), q2 = pair_word(bb, 2, k),
@@ -443,67 +487,81 @@ __global__ void __launch_bounds__(kP4Threads, 1) prefill_int4_kernel(PrefillArgs
                 const uint4& q = fv.w[bb][mt >> 2];
                 const uint32_t w = (mt & 3) == 0 ? q.x : (mt & 3) == 1 ? q.y : (mt & 3) == 2 ? q.z : q.w;
                 const uint32_t y = w >> 8;  // tokens 1 and 3
-                uint32_t e02 = p4_even(w, s02, m02), e13 = p4_even(y, s13, m13);
-                uint32_t o02 = p4_odd(w, s02, m02), o13 = p4_odd(y, s13, m13);
-                if constexpr (decltype(sat)::value) {
-                  e02 = sat_h2(e02); e13 = sat_h2(e13);
-                  o02 = sat_h2(o02); o13 = sat_h2(o13);
-                }
-                put(16 * mt + 2 * vg, e02, e13);
-                put(16 * mt + 2 * vg + 1, o02, o13);
+                put(bb, 16 * mt + 2 * vg, p4_even(w, s02, m02), p4_even(y, s13, m13));
+                put(bb, 16 * mt + 2 * vg + 1, p4_odd(w, s02, m02), p4_odd(y, s13, m13));
               }
             }
-          };
-          if (__builtin_expect(big, 0)) convert(std::true_type{});
-          else convert(std::false_type{});
-        } else {
-          const int p = quad_pos(c, bb);
-          int src[4];
-#pragma unroll
-          for (int t = 0; t < 4; ++t) {
-            const int pt = p + t;
-            src[t] = fv.src[bb] == 0 || pt > pmax || pt >= a.L        ? 0
-                     : (pt < a.nsink || pt >= a.L - kWin) ? 2
-                     : fv.src[bb] == 3                    ? 1
-                                                          : 0;
-          }
-#pragma unroll
-          for (int mt = 0; mt < 8; ++mt) {
-            const uint4& q = fv.w[bb][mt >> 2];
-            const uint32_t w = (mt & 3) == 0 ? q.x : (mt & 3) == 1 ? q.y : (mt & 3) == 2 ? q.z : q.w;
-            uint32_t e[4];  // token t: channels 16 mt + 2 vg, + 1
-#pragma unroll
-            for (int t = 0; t < 4; ++t) {
-              e[t] = 0u;
-              if (src[t] == 2) {
-                e[t] = *reinterpret_cast<const uint32_t*>(fp16_row(p + t, 1) + 16 * mt + 2 * vg);
-              } else if (src[t] == 1) {
-                const __half2 sm = bits_h2(pair_word(bb, t, mt * NG / 8));
-                const uint32_t byte = (w >> (8 * t)) & 0xFFu;
-                e[t] = sat_h2(p4_even((byte & 15u) | (byte << 12), __low2half2(sm), __high2half2(sm)));
-              }
-            }
-            put(16 * mt + 2 * vg, __byte_perm(e[0], e[2], 0x5410u), __byte_perm(e[1], e[3], 0x5410u));
-            put(16 * mt + 2 * vg + 1, __byte_perm(e[0], e[2], 0x7632u), __byte_perm(e[1], e[3], 0x7632u));
+          } else {
+            rare |= 1u << bb;
           }
         }
-      }
-      um_fence_proxy_async();
-      mbar_arrive(&ms.v_full[st]);
-      // The next chunk's loads go out here, behind the second fence: a fence
-      // waits for the loads in flight, so keys fetched between the two fences
-      // (and values before the first) left their latency bare twice per chunk.
-      if (i + 1 < n) {
-        fetch_k(c + 1, kblk);
-        fetch_v(c + 1, vblk);
-        kblk = block_of(kP4Keys * (c + 2) + kt);
+        if (__builtin_expect(rare != 0, 0)) {
+#pragma unroll 1
+          for (int bb = 0; bb < 2; ++bb) {
+            if (((rare >> bb) & 1u) == 0) continue;
+            const int p = quad_pos(c, bb), src = bb == 0 ? fv.src[0] : fv.src[1];
+            const __half* row[4];  // of the quad's tokens: fp16 rows, null for codes and for tokens nobody reads
 #pragma unroll
-        for (int bb = 0; bb < 2; ++bb) vblk[bb] = block_of(quad_pos(c + 2, bb));
+            for (int t = 0; t < 4; ++t) {
+              const int pt = p + t;
+              const bool fp16 = src != 0 && pt <= pmax && pt < a.L && (pt < a.nsink || pt >= a.L - kWin);
+              row[t] = fp16 ? fp16_row(pt, 1) : nullptr;
+            }
+            if ((src & 1) == 0) {  // no codes: 8 channels of the four rows at a time
+#pragma unroll 1
+              for (int h = 0; h < 128; h += 64) {
+                const int ch = h + 8 * vg;
+                uint4 y[4];
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+                  y[t] = row[t] != nullptr ? *reinterpret_cast<const uint4*>(row[t] + ch) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  const uint32_t e0 = (&y[0].x)[k], e1 = (&y[1].x)[k], e2 = (&y[2].x)[k], e3 = (&y[3].x)[k];
+                  put(bb, ch + 2 * k, __byte_perm(e0, e2, 0x5410u), __byte_perm(e1, e3, 0x5410u));
+                  put(bb, ch + 2 * k + 1, __byte_perm(e0, e2, 0x7632u), __byte_perm(e1, e3, 0x7632u));
+                }
+              }
+              continue;
+            }
+            // codes beside fp16 rows, or values that saturate: token by token
+            const uint8_t* bp = head_of(__ldg(table + (p >> 4)));
+#pragma unroll 1
+            for (int mt = 0; mt < 8; ++mt) {
+              const uint8_t* wp = bp + kVcOff4 + (mt >> 2) * 512 + 16 * lane + 4 * (mt & 3);
+              const uint32_t w = *reinterpret_cast<const uint32_t*>(wp);
+              uint32_t e[4];  // token t: channels 16 mt + 2 vg, + 1
+#pragma unroll
+              for (int t = 0; t < 4; ++t) {
+                const uint8_t* mp = bp + kSm + 64 * NG + ((4 * tq + t) * NG + mt * NG / 8) * 4;
+                const __half2 sm = *reinterpret_cast<const __half2*>(mp);
+                const uint32_t byte = (w >> (8 * t)) & 0xFFu;
+                e[t] = sat_h2(p4_even((byte & 15u) | (byte << 12), __low2half2(sm), __high2half2(sm)));
+                if (row[t] != nullptr) e[t] = *reinterpret_cast<const uint32_t*>(row[t] + 16 * mt + 2 * vg);
+                else if (p + t > pmax || p + t >= a.L) e[t] = 0u;
+              }
+              put(bb, 16 * mt + 2 * vg, __byte_perm(e[0], e[2], 0x5410u), __byte_perm(e[1], e[3], 0x5410u));
+              put(bb, 16 * mt + 2 * vg + 1, __byte_perm(e[0], e[2], 0x7632u), __byte_perm(e[1], e[3], 0x7632u));
+            }
+          }
+        }
+        um_fence_proxy_async();
+        mbar_arrive(&ms.v_full[st]);
+        // The next chunk's loads go out here, behind the second fence: a fence
+        // waits for the loads in flight, so keys fetched between the two fences
+        // (and values before the first) left their latency bare twice per chunk.
+        if (i + 1 < pc.n) {
+          fetch_k(c + 1, kblk);
+          fetch_v(c + 1, vblk);
+          kblk = block_of(kP4Keys * (c + 2) + kt);
+#pragma unroll
+          for (int bb = 0; bb < 2; ++bb) vblk[bb] = block_of(quad_pos(c + 2, bb));
+        }
       }
     }
   } else {
     // ------------------------------------------------------------ MMA issue
-    // S_0(0), S_1(0), then per chunk: O_0 += P_0 V, S_0 of the next chunk, O_1 += P_1 V, S_1 of the next.
+    // Per piece S_0(0), S_1(0), then per chunk: O_0 += P_0 V, S_0 of the next chunk, O_1 += P_1 V, S_1 of the next.
     // The whole warp runs the loop and one elected lane issues: descriptors and
     // TMEM addresses then stay in uniform registers.  (Issued by `lane == 0`,
     // an MMA cost the thread 130 cycles, twice its time on the tensor pipe.)
@@ -511,12 +569,17 @@ __global__ void __launch_bounds__(kP4Threads, 1) prefill_int4_kernel(PrefillArgs
     uint32_t last_par = 0;
     const uint64_t dQ = um_desc(base + kP4OffQ), dK = um_desc(base + kP4OffK), dV = um_desc(base + kP4OffV);
     // phase `k` of a barrier, the same answer in every lane
-    auto wait = [&](uint64_t* bar, int k) { return __all_sync(0xffffffffu, mbar_wait_bounded(bar, (uint32_t)k & 1u)) != 0; };
+    auto wait = [&](uint64_t* bar, int k) {
+      return __all_sync(0xffffffffu, mbar_wait_bounded(bar, (uint32_t)k & 1u)) != 0;
+    };
+    int nt = 0;
+    int done = 0, seen[2] = {0, 0}, pieces[2] = {0, 0};  // before this piece: chunks; those, and pieces, with tile t
     auto issue_s = [&](int t, int i) -> bool {
-      const int st = i & 1;
-      if (!wait(&ms.k_full[st], i >> 1)) return false;
+      const int at = done + i, st = at & 1, own = (t == 0 ? seen[0] : seen[1]) + i;
+      if (!wait(&ms.k_full[st], at >> 1)) return false;
       // the weights of the chunk before lie over the score columns until its value MMA is done
-      if (i >= 1 && !wait(&ms.pv_done[t], i - 1)) return false;
+      if (own >= 1 && !wait(&ms.pv_done[t], own - 1)) return false;
+      if (i == 0 && !wait(&ms.q_full[t], t == 0 ? pieces[0] : pieces[1])) return false;
       um_fence_after();
       const uint64_t qd = dQ + (uint64_t)((t * kP4Tile) >> 4), kd = dK + (uint64_t)((st * kP4Tile) >> 4);
       if (um_elect()) {
@@ -531,13 +594,13 @@ __global__ void __launch_bounds__(kP4Threads, 1) prefill_int4_kernel(PrefillArgs
       }
       __syncwarp();
       last_bar = t == nt - 1 ? &ms.k_free[st] : &ms.s_full[t];
-      last_par = (uint32_t)(t == nt - 1 ? i >> 1 : i) & 1u;
+      last_par = (uint32_t)(t == nt - 1 ? at >> 1 : own) & 1u;
       return true;
     };
     auto issue_pv = [&](int t, int i) -> bool {
-      const int st = i & 1;
-      if (!wait(&ms.v_full[st], i >> 1)) return false;
-      if (!wait(&ms.p_full[t], i)) return false;
+      const int at = done + i, st = at & 1, own = (t == 0 ? seen[0] : seen[1]) + i;
+      if (!wait(&ms.v_full[st], at >> 1)) return false;
+      if (!wait(&ms.p_full[t], own)) return false;
       um_fence_after();
       const uint64_t vd = dV + (uint64_t)((st * kP4Tile) >> 4);
       if (um_elect()) {
@@ -552,14 +615,26 @@ __global__ void __launch_bounds__(kP4Threads, 1) prefill_int4_kernel(PrefillArgs
       }
       __syncwarp();
       last_bar = t == nt - 1 ? &ms.v_free[st] : &ms.pv_done[t];
-      last_par = (uint32_t)(t == nt - 1 ? i >> 1 : i) & 1u;
+      last_par = (uint32_t)(t == nt - 1 ? at >> 1 : own) & 1u;
       return true;
     };
     bool alive = true;
-    for (int t = 0; t < nt && alive && n > 0; ++t) alive = issue_s(t, 0);
-    for (int i = 0; i < n && alive; ++i)
-      for (int t = 0; t < nt && alive; ++t)
-        alive = issue_pv(t, i) && (i + 1 >= n || issue_s(t, i + 1));
+    Piece pc;
+#pragma unroll 1
+    for (int2 u = u_begin; more(u) && alive;) {
+      u = next_piece(u, pc);
+      nt = pc.nt;
+#pragma unroll 1
+      for (int i = -1; i < pc.n && alive; ++i)
+#pragma unroll 1
+        for (int t = 0; t < nt && alive; ++t)
+          alive = (i < 0 || issue_pv(t, i)) && (i + 1 >= pc.n || issue_s(t, i + 1));
+      done += pc.n;
+      for (int t = 0; t < nt; ++t) {
+        (t == 0 ? seen[0] : seen[1]) += pc.n;
+        (t == 0 ? pieces[0] : pieces[1]) += 1;
+      }
+    }
     if (!alive && lane == 0) raise_flag(a.status, OKV_DEV_TIMEOUT);
     // the MMAs already issued finish before TMEM is freed: the last commit covers them all
     if (last_bar != nullptr) mbar_drain_bounded(last_bar, last_par);
@@ -574,16 +649,15 @@ __global__ void __launch_bounds__(kP4Threads, 1) prefill_int4_kernel(PrefillArgs
 
 }  // namespace
 
-okv_status launch_prefill_int4_bf16(const PrefillArgs& a, cudaStream_t s) {
-  using Kernel = void (*)(PrefillArgs);
+okv_status launch_prefill_int4_bf16(const PrefillArgs& a, const P4Split& sp, cudaStream_t s) {
+  using Kernel = void (*)(PrefillArgs, P4Split);
   static const Kernel kernels[3] = {prefill_int4_kernel<1>, prefill_int4_kernel<2>, prefill_int4_kernel<4>};
   static std::atomic<uint32_t> attr[3];
   const int gi = a.ng >> 1;  // ng = 1, 2, 4 -> 0, 1, 2
   const cudaError_t e = set_smem_limit_once((const void*)kernels[gi], (int)kP4Smem, attr[gi]);
   if (e != cudaSuccess) return fail(OKV_ERR_CUDA, "prefill attention smem attribute: %s", cudaGetErrorString(e));
-  const dim3 grid((unsigned)((a.T * a.g + kP4Rows - 1) / kP4Rows), (unsigned)a.hkv, (unsigned)a.splits);
   // (a programmatic launch behind the query rotation measured no faster: 885 against 871 us)
-  kernels[gi]<<<grid, kP4Threads, kP4Smem, s>>>(a);
+  kernels[gi]<<<sp.ctas, kP4Threads, kP4Smem, s>>>(a, sp);
   return check_launch("prefill attention");
 }
 
