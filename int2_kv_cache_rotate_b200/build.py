@@ -19,7 +19,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libokv.so")
 SHORT_WAIT_LIB = os.path.join(HERE, "libokv_shortwait.so")
-SOURCES = ["okv_api.cu", "append.cu", "decode.cu", "decode_int4.cu", "dequant.cu", "prefill.cu", "prefill_int4.cu",
+SOURCES = ["okv_api.cu", "append.cu", "decode.cu", "decode_int4.cu", "dequant.cu", "prefill.cu", "prefill_int4.cu", "prefill_rotate.cu",
            "noalloc.cu", "plan.cu", "norm_rope.cu", "calib.cpp", "rotio.cpp"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 

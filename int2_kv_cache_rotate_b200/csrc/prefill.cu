@@ -1298,8 +1298,13 @@ okv_status launch_prefill(const okv_cache_desc* d, const void* q, int T, int slo
   if (e0 != cudaSuccess) return fail(OKV_ERR_CUDA, "prefill rotation smem attribute: %s", cudaGetErrorString(e0));
   const int rt_cta_rows = small ? rt_rows(2) : rt_rows(8);
   const dim3 rt_grid((unsigned)((T * a.g + rt_cta_rows - 1) / rt_cta_rows), (unsigned)a.hkv);
-  qrot<<<rt_grid, 256, rt_bytes, s>>>(a);
-  okv_status st = check_launch("prefill query rotation");
+  okv_status st;
+  if (int4_bf16 && d->r_image != nullptr) {
+    st = launch_prefill_qrot_int4(a, d->r_image, s);
+  } else {
+    qrot<<<rt_grid, 256, rt_bytes, s>>>(a);
+    st = check_launch("prefill query rotation");
+  }
   if (st != OKV_OK) return st;
   P4Split sp{};
   if (int4_bf16) {
@@ -1319,6 +1324,7 @@ okv_status launch_prefill(const okv_cache_desc* d, const void* q, int T, int slo
     st = check_launch("prefill attention");
   }
   if (st != OKV_OK) return st;
+  if (int4_bf16 && !small && (uintptr_t)out % 16 == 0) return launch_prefill_unrotate_int4(a, sp, s);
   // The un-rotation may start (programmatic launch) while the attention's last
   // CTAs run: it stages U_V, then waits for the attention's outputs.  Starting
   // the attention early behind the query rotation in the same way measured

@@ -73,4 +73,9 @@ __host__ __device__ inline int prefill_last_pos(const PrefillArgs& a, int x) {  
 }
 okv_status launch_prefill_int4_bf16(const PrefillArgs& a, const P4Split& sp, cudaStream_t s);
 
+// Its rotations on the tensor cores (prefill_rotate.cu): q~ from the cache's
+// staged image of R, and the output (16-byte aligned) from U_V.
+okv_status launch_prefill_qrot_int4(const PrefillArgs& a, const void* r_image, cudaStream_t s);
+okv_status launch_prefill_unrotate_int4(const PrefillArgs& a, const P4Split& sp, cudaStream_t s);
+
 }  // namespace okv

@@ -500,3 +500,55 @@ def test_chunked_prefill_rows_keep_apart(group):
     keep = torch.ones(90, 8, dtype=torch.bool, device="cuda")
     keep[33, 5] = False
     assert torch.equal(got[keep], out[keep])
+
+
+@pytest.mark.parametrize("group", [128, 32])
+@pytest.mark.parametrize("hq,hkv,length,tokens", [(32, 8, 700, 300), (40, 2, 1333, 251), (64, 64, 400, 390), (6, 2, 2100, 2100)])
+@pytest.mark.parametrize("stage_r,off", [(True, 0), (False, 0), (True, 3)])
+def test_chunked_prefill_with_many_rows(group, hq, hkv, length, tokens, stage_r, off):
+    """Chunks whose rotations run on the tensor cores, without the staged image of R, and into an output off 16
+    bytes (both take the other rotations): every row against 64 bits, rows in front of the output untouched."""
+    okv = _okv()
+    gc, oc, lay, _ = fill(41, hq, hkv, [length], group, sinks=16, stage_r=stage_r)
+    q, qn = queries(41, tokens, hq, hkv)
+    buf = torch.full((off + tokens * hq * 128 + 8,), 7.0, dtype=torch.bfloat16, device="cuda")
+    out = buf[off:off + tokens * hq * 128].view(tokens, hq, 128)
+    okv.prefill_attention(gc, q, 0, length, _t(lay.table), out=out)
+    assert gc.device_status() == 0
+    assert (buf[:off] == 7).all() and (buf[off + tokens * hq * 128:] == 7).all()
+    got = out.float().cpu().numpy()
+    seen = np.arange(length)[None] <= np.arange(length - tokens, length)[:, None]
+    for h in range(hkv):
+        keys, vals = (oc.values(0, kind, h, length) for kind in (0, 1))
+        for j in range(h * hq // hkv, (h + 1) * hq // hkv):
+            x = np.where(seen, (qn[:, j].astype(np.float64) @ oc.r[0][h]) @ keys.T / math.sqrt(128), -np.inf)
+            w = np.exp(x - x.max(1, keepdims=True))
+            check_rows(got[:, j], (w / w.sum(1, keepdims=True)) @ vals @ oc.r[1][h].T, TOL + 2.0 ** -8)
+
+
+def test_chunked_prefill_with_many_rows_scales_and_keeps_rows_apart():
+    """Values times 2^k give the output times 2^k: a row's scale leaves nothing of its 2^-12 to the values' size.
+    An infinite query row leaves the others alone."""
+    okv = _okv()
+    outs = []
+    for k in (0, -9, 10):
+        def put(kind, b, z):
+            if kind == 1:
+                z *= 2.0 ** k
+        gc, oc, lay, _ = fill(42, 32, 8, [500], 128, extra=put)
+        q, _ = queries(42, 310, 32, 8)
+        outs.append(torch.empty(310, 32, 128, dtype=torch.bfloat16, device="cuda"))
+        okv.prefill_attention(gc, q, 0, 500, _t(lay.table), out=outs[-1])
+        assert gc.device_status() == 0
+    # 2^-9: (scale, min) pairs and fp16 rows near 2^-9 keep 11 bits down to 2^-14, a unit of 2^-24 below: against
+    # rows of norm ~2^-9 their rounding is 2^-15 a value; both bf16 outputs round by 2^-9, values and weights 2^-11
+    for o, k in zip(outs[1:], (-9, 10)):
+        a, b = outs[0].double(), o.double() * 2.0 ** -k
+        assert ((a - b).norm(dim=-1) / a.norm(dim=-1)).max() <= 2 * 2.0 ** -9 + 2.0 ** -8
+    bad = q.clone()
+    bad[77, 9, 3] = float("inf")
+    got = torch.empty_like(outs[-1])
+    okv.prefill_attention(gc, bad, 0, 500, _t(lay.table), out=got)
+    keep = torch.ones(310, 32, dtype=torch.bool, device="cuda")
+    keep[77, 9] = False
+    assert torch.equal(got[keep], outs[-1][keep])

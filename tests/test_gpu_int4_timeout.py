@@ -59,3 +59,15 @@ def test_four_bit_timeouts_wind_down_cleanly():
     from int2_kv_cache_rotate_b200 import okv
     flags = [int(x) for x in line.split()[1:]]
     assert len(flags) == 10 and all(s & okv.DEV_TIMEOUT for s in flags), flags
+
+
+def test_four_bit_prefill_of_many_rows_winds_down_cleanly():
+    """400 x 32 rows: the rotations' own waits run out as well."""
+    child = CHILD.replace("(256, hq, 128)", "(400, hq, 128)").replace("for T in (256, 16):", "for T in (400, 300):")
+    env = dict(os.environ, OKV_LIBRARY=_short_wait_lib(), PYTHONPATH=ROOT + os.pathsep + os.environ.get("PYTHONPATH", ""))
+    res = subprocess.run([sys.executable, "-c", child], cwd=ROOT, env=env, capture_output=True, text=True, timeout=600)
+    assert res.returncode == 0, res.stdout + res.stderr
+    line = [ln for ln in res.stdout.splitlines() if ln.startswith("STATUS")][-1]
+    from int2_kv_cache_rotate_b200 import okv
+    flags = [int(x) for x in line.split()[1:]]
+    assert len(flags) == 10 and all(s & okv.DEV_TIMEOUT for s in flags), flags
