@@ -157,7 +157,9 @@ typedef struct {
                                  every (KV head, K|V), written by
                                  okv_build_r_image for the current u_k, u_v
                                  (rebuild it after changing them).  NULL: each
-                                 prefill append stages R itself.           */
+                                 prefill append stages R itself, and a 4-bit
+                                 prefill with bf16 output rotates its queries
+                                 on the CUDA cores (slower).               */
 } okv_cache_desc;
 
 /* Offline calibration of the rotations, on the host in fp64 (once per layer).

@@ -36,10 +36,14 @@
 // columns and in the value tile alike.
 // Bound: 128 keys x 256 rows cost 32 MMAs of 64 cycles and 32768 exponentials
 // at 16 a cycle, 2048 cycles each; a chunk takes 5250 (1024 tokens over 32K keys,
-// 32/8 heads: 640 us, 860 TFLOP/s), the exponential unit and the tensor pipe
+// 32/8 heads: 640 us, 845 TFLOP/s), the exponential unit and the tensor pipe
 // 39 % busy, issue slots 45 %: what is left is the latency of each tile's chain
 // of scores, softmax and value MMA.  One range of work per SM against one tile
-// per CTA (128 of them): 762 against 873 us a call.
+// per CTA (128 of them): 762 against 873 us a call.  Not taken (same call, 762):
+// the value MMA of the first 64 keys started while the softmax does the others
+// 847 (the issuing warp then waits where the other tile could go on), a warp of
+// MMAs per tile 785 (the tiles fall into step), both 785, the next batch's
+// scores loaded ahead 768.
 #include <type_traits>
 
 #include "okv_common.cuh"

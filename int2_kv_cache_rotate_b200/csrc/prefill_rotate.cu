@@ -11,8 +11,11 @@
 //   output the merged row is normalised, goes through the butterfly in
 //          registers in fp32 and, scaled by 2^-e, to fp16 (2^-12 of a value,
 //          an eighth of a bf16 output's rounding), B = U_V as two fp16 parts.
-// Bound: bytes (32768 rows: 17 MB in and out before, 25 to 50 MB behind the
-// attention) and the latency of load, product and store one after the other.
+// Bound: the latency of load, product and store one after the other, and behind
+// the attention the bytes (32768 rows: 17 MB, and up to three pieces of each).
+// 32768 rows take 10 us before the attention (39 on the CUDA cores) and 35
+// behind it (45 and more); fp32 output and the 2-bit cache keep the CUDA cores,
+// whose fp32 products their smaller tolerances count on.
 #include "okv_common.cuh"
 #include "okv_internal.h"
 #include "prefill_common.cuh"
