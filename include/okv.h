@@ -336,10 +336,11 @@ okv_status okv_decode_attention_noalloc(const okv_cache_desc* desc, const void* 
  * decode, q~ = q R_K and o = softmax(q~ x^T / sqrt(d)) x_V R_V^T.
  *   q: device bf16 [T][Hq][d], 16-byte aligned; slot, context_len: host ints (T <= L <=
  *   max_blocks_per_seq * 16); block_table: device, as above; out: device
- *   fp32 [T][Hq][d]; workspace: device, at least
- *   okv_prefill_workspace_bytes(desc, T) bytes, 256-B aligned (the same for
- *   either output type; a short chunk over 4-bit codes is split over key
- *   ranges, whose partial results it holds).
+ *   fp32 [T][Hq][d], or bf16 (16-byte aligned: the faster un-rotation);
+ *   workspace: device, at least okv_prefill_workspace_bytes(desc, T) bytes,
+ *   256-B aligned (the same for either output type; over 4-bit codes it also
+ *   holds the partial results of row tiles that two or more SMs share the keys
+ *   of, at most two pieces of 256 rows per SM, 40 MB).
  * Three launches on `stream` (query rotation, attention on the tensor cores,
  * normalisation and value un-rotation).  Errors: INVALID_ARG (NULL, sizes,
  * slot or context_len out of range, workspace too small); block ids outside

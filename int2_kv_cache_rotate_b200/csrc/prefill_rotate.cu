@@ -167,8 +167,6 @@ __global__ void __launch_bounds__(256, 2)
     mbar_init(&ctl.done, 1);
     fence_mbar_init();
   }
-  __syncwarp();
-  if (warp == 0) um_alloc(&ctl.tmem_slot, 128);
   {
     // B = U_V, row i K-major: 8 channels of a row per piece, hi and lo
     const float4* U = reinterpret_cast<const float4*>(a.u_v + (size_t)hk * kD * kD);
@@ -200,6 +198,7 @@ __global__ void __launch_bounds__(256, 2)
     }
   }
   grid_dep_wait();  // the attention's outputs are read from here on
+  if (warp == 0) um_alloc(&ctl.tmem_slot, 128);  // (behind the wait: no CTA holds TMEM while it waits for a grid)
   const int t0 = r0 / kP4Rows * kP4Rows;
   int pieces;
   const int j0 = sp.ranges_of(hk * sp.tiles + r0 / kP4Rows, pieces);

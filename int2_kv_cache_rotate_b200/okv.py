@@ -349,6 +349,13 @@ def decode_workspace_bytes(cache: Cache, batch: int) -> int:
     return int(lib().okv_decode_workspace_bytes(ctypes.byref(cache.desc), batch))
 
 
+def _scratch(t, stream):
+    """A workspace that a call makes for itself: its memory is not handed out again before `stream` is past the call."""
+    if stream is not None:
+        t.record_stream(stream)
+    return t
+
+
 def workspace(cache: Cache, batch: int):
     return _t().empty(max(decode_workspace_bytes(cache, batch), 256), dtype=_torch.uint8, device=cache.pages.device)
 
@@ -366,13 +373,13 @@ def decode_attention(cache: Cache, q, seq_slot, block_table, context_lens, out=N
     B, seq, table, ctx = _decode_args(cache, q, seq_slot, block_table, context_lens)
     out, desc = _out(cache, out, B, q.device)
     if ws is None:
-        ws = workspace(cache, B)
+        ws = _scratch(workspace(cache, B), stream)
     _run(q, stream, lib().okv_decode_attention, ctypes.byref(desc), q.data_ptr(), B, seq, table, ctx, out.data_ptr(),
          ws.data_ptr(), ws.numel())
     return out
 
 
-def _step_args(cache, k, v, new_seq_slot, new_pos, slot_lens, q, seq_slot, block_table, context_lens, out, ws):
+def _step_args(cache, k, v, new_seq_slot, new_pos, slot_lens, q, seq_slot, block_table, context_lens, out, ws, stream):
     """Output, the library's arguments but for the stream, and what they point into."""
     bf16 = _t().bfloat16
     _need(k, bf16, "k"), _need(v, bf16, "v"), _need(q, bf16, "q")
@@ -387,7 +394,7 @@ def _step_args(cache, k, v, new_seq_slot, new_pos, slot_lens, q, seq_slot, block
         _ints(block_table, "block_table", slots * cache.max_blocks_per_seq)
     out, desc = _out(cache, out, B, q.device)
     if ws is None:
-        ws = workspace(cache, B)
+        ws = _scratch(workspace(cache, B), stream)
     args = (ctypes.byref(desc), k.data_ptr(), v.data_ptr(), T, _ints(new_seq_slot, "new_seq_slot", T),
             _ints(new_pos, "new_pos", T), _ints(slot_lens, "slot_lens", slots), q.data_ptr(), B, seq, table, ctx,
             out.data_ptr(), ws.data_ptr(), ws.numel())
@@ -398,7 +405,7 @@ def decode_step(cache: Cache, k, v, new_seq_slot, new_pos, slot_lens, q, seq_slo
                 out=None, ws=None, stream=None):
     """Append this step's bf16 tokens, then decode (one call; see okv_decode_step); out: fp32 or bf16 [B, Hq, 128]."""
     out, args, _ = _step_args(cache, k, v, new_seq_slot, new_pos, slot_lens, q, seq_slot, block_table, context_lens,
-                              out, ws)
+                              out, ws, stream)
     _run(q, stream, lib().okv_decode_step, *args)
     return out
 
@@ -415,7 +422,7 @@ class DecodeStepCall:
     def __init__(self, cache: Cache, k, v, new_seq_slot, new_pos, slot_lens, q, seq_slot, block_table,
                  context_lens, out=None, ws=None, stream=None, graph: bool = False):
         self.out, self._args, keep = _step_args(cache, k, v, new_seq_slot, new_pos, slot_lens, q, seq_slot, block_table,
-                                                context_lens, out, ws)
+                                                context_lens, out, ws, stream)
         self._keep = (cache, k, v, new_seq_slot, new_pos, slot_lens, q, seq_slot, block_table, context_lens, keep)
         self._fn = lib().okv_decode_step
         self._stream = stream
@@ -466,7 +473,8 @@ def prefill_attention(cache: Cache, q, slot: int, context_len: int, block_table,
     table = _ints(block_table, "block_table", cache.num_seq_slots * cache.max_blocks_per_seq if T else 0)
     out, desc = _out(cache, out, T, q.device)
     if ws is None:
-        ws = _torch.empty(max(prefill_workspace_bytes(cache, T), 256), dtype=_torch.uint8, device=q.device)
+        ws = _scratch(_torch.empty(max(prefill_workspace_bytes(cache, T), 256), dtype=_torch.uint8, device=q.device),
+                      stream)
     _run(q, stream, lib().okv_prefill_attention, ctypes.byref(desc), q.data_ptr(), T, int(slot), int(context_len),
          table, out.data_ptr(), ws.data_ptr(), ws.numel())
     return out

@@ -552,3 +552,23 @@ def test_chunked_prefill_with_many_rows_scales_and_keeps_rows_apart():
     keep = torch.ones(310, 32, dtype=torch.bool, device="cuda")
     keep[77, 9] = False
     assert torch.equal(got[keep], outs[-1][keep])
+
+
+@pytest.mark.parametrize("val", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("where", [5, 100, 260])   # a sink row, codes, the window
+@pytest.mark.parametrize("kind", [0, 1])
+def test_chunked_prefill_rows_before_a_token_that_is_not_finite(val, where, kind):
+    """The cache holds such a token's channel as zero or at fp16's end, so it reaches nobody through the mask."""
+    okv = _okv()
+
+    def put(k, b, z):
+        if k == kind:
+            z[where, 1, 17] = val
+    outs = []
+    for extra in (None, put):
+        gc, _, lay, _ = fill(45, 8, 2, [300], 64, sinks=16, extra=extra)
+        q, _ = queries(45, 300, 8, 2)
+        outs.append(torch.empty(300, 8, 128, dtype=torch.bfloat16, device="cuda"))
+        okv.prefill_attention(gc, q, 0, 300, _t(lay.table), out=outs[-1])
+    assert torch.equal(outs[0][:where], outs[1][:where]) and torch.equal(outs[0][:, :4], outs[1][:, :4])
+    assert torch.isfinite(outs[1]).all()
