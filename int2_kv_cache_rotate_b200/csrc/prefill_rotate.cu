@@ -74,6 +74,7 @@ __global__ void __launch_bounds__(128, 2) prefill_qrot_int4_kernel(const __grid_
   RoCtl& ctl = *reinterpret_cast<RoCtl*>(gb + kRoOffCtl);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int hk = blockIdx.y, nrows = a.T * a.g, r0 = blockIdx.x * kRoRows;
+  grid_dep_launch();  // the attention may start fetching codes
   if (tid == 0) {
     mbar_init(&ctl.b_full, 1);
     mbar_init(&ctl.done, 1);
