@@ -194,7 +194,11 @@ def _need(t, dtype, name, device=True):
 
 def _heads(t, dtype, name, heads):
     """t: contiguous [rows][heads][128] on a GPU; returns its rows (none needs no shape)."""
-    _need(t, dtype, name)
+    return _rows(_need(t, dtype, name), name, heads)
+
+
+def _rows(t, name, heads):
+    """The rows of a tensor that _need has passed."""
     shape = t.shape
     if len(shape) == 3 and shape[1] == heads and shape[2] == HEAD_DIM:
         return shape[0]
@@ -360,9 +364,16 @@ def workspace(cache: Cache, batch: int):
     return _t().empty(max(decode_workspace_bytes(cache, batch), 256), dtype=_torch.uint8, device=cache.pages.device)
 
 
+def _least(t, name, least):
+    """The address of an integer tensor that _need has passed, with `least` values or more."""
+    if t.numel() < least:
+        raise ValueError(f"{name} must hold at least {least} values, got {t.numel()}")
+    return t.data_ptr()
+
+
 def _decode_args(cache, q, seq_slot, block_table, context_lens):
-    """Rows of q, and the pointers of a decode call's integer arrays."""
-    B = _heads(q, _t().bfloat16, "q", cache.hq)
+    """Rows of q (which _need has passed), and the pointers of a decode call's integer arrays."""
+    B = _rows(q, "q", cache.hq)
     slots = cache.num_seq_slots if B else 0
     return (B, _ints(seq_slot, "seq_slot", B), _ints(block_table, "block_table", slots * cache.max_blocks_per_seq),
             _ints(context_lens, "context_lens", B))
@@ -370,6 +381,7 @@ def _decode_args(cache, q, seq_slot, block_table, context_lens):
 
 def decode_attention(cache: Cache, q, seq_slot, block_table, context_lens, out=None, ws=None, stream=None):
     """Decode attention of one query per sequence; out: fp32 (a new tensor when None) or bf16 [B, Hq, 128]."""
+    _need(q, _t().bfloat16, "q")
     B, seq, table, ctx = _decode_args(cache, q, seq_slot, block_table, context_lens)
     out, desc = _out(cache, out, B, q.device)
     if ws is None:
@@ -386,8 +398,8 @@ def _step_args(cache, k, v, new_seq_slot, new_pos, slot_lens, q, seq_slot, block
     for name, t in (("new_seq_slot", new_seq_slot), ("new_pos", new_pos), ("slot_lens", slot_lens)):
         _need(t, _torch.int32, name)
     B, seq, table, ctx = _decode_args(cache, q, seq_slot, block_table, context_lens)
-    T = _heads(k, bf16, "k", cache.hkv)
-    if _heads(v, bf16, "v", cache.hkv) != T:
+    T = _rows(k, "k", cache.hkv)
+    if _rows(v, "v", cache.hkv) != T:
         raise ValueError("k and v must have the same number of rows")
     slots = cache.num_seq_slots if T else 0
     if T and not B:
@@ -395,8 +407,8 @@ def _step_args(cache, k, v, new_seq_slot, new_pos, slot_lens, q, seq_slot, block
     out, desc = _out(cache, out, B, q.device)
     if ws is None:
         ws = _scratch(workspace(cache, B), stream)
-    args = (ctypes.byref(desc), k.data_ptr(), v.data_ptr(), T, _ints(new_seq_slot, "new_seq_slot", T),
-            _ints(new_pos, "new_pos", T), _ints(slot_lens, "slot_lens", slots), q.data_ptr(), B, seq, table, ctx,
+    args = (ctypes.byref(desc), k.data_ptr(), v.data_ptr(), T, _least(new_seq_slot, "new_seq_slot", T),
+            _least(new_pos, "new_pos", T), _least(slot_lens, "slot_lens", slots), q.data_ptr(), B, seq, table, ctx,
             out.data_ptr(), ws.data_ptr(), ws.numel())
     return out, args, (desc, ws)
 
@@ -454,6 +466,7 @@ class DecodeStepCall:
 
 def decode_attention_noalloc(cache: Cache, q, seq_slot, block_table, context_lens, out=None, stream=None):
     """Decode attention with the library's static scratch (no workspace, no allocation in the library)."""
+    _need(q, _t().bfloat16, "q")
     B, seq, table, ctx = _decode_args(cache, q, seq_slot, block_table, context_lens)
     out, desc = _out(cache, out, B, q.device)
     _run(q, stream, lib().okv_decode_attention_noalloc, ctypes.byref(desc), q.data_ptr(), B, seq, table, ctx,
