@@ -77,6 +77,7 @@ class NormRopeArgs(ctypes.Structure):
 
 # the same two structures as bytes, for calls that fill every field at once
 _PLAN, _ROPE = struct.Struct("5i4x13P"), struct.Struct("8i2f3P6q7P")
+_WEIGHT = (HEAD_DIM,)
 assert _PLAN.size == ctypes.sizeof(PlanArgs) and _ROPE.size == ctypes.sizeof(NormRopeArgs)
 
 _lib = None
@@ -557,6 +558,38 @@ class AppendPlan:
         self.status.zero_()
 
 
+def _rope_refuse(q, k, v, positions, inv_freq, weights, outs):
+    """The error of a qk_norm_rope call whose tensors do not fit, found one by one."""
+    torch = _t()
+    dt, dev = q.dtype, q.get_device()
+    if dt not in (torch.bfloat16, torch.float16, torch.float32):
+        raise TypeError(f"q must be bfloat16, float16 or float32, got {dt}")
+    given = [(n, t) for n, t in (("q", q), ("k", k), ("v", v)) if t is not None]
+    for name, t in given:
+        if t.dtype is not dt:
+            raise TypeError(f"{name} must be {dt} like q, got {t.dtype}")
+    for name, t in given:
+        if dev < 0 or t.get_device() != dev:
+            raise ValueError(f"{name} must be a CUDA tensor on one device with q")
+        if t.dim() != 3 or t.shape[2] != HEAD_DIM or t.stride(2) != 1 or t.shape[0] != q.shape[0]:
+            raise ValueError(f"{name} must be [T][heads][{HEAD_DIM}] with contiguous rows, got {tuple(t.shape)}")
+    if v is not None and v.shape[1] != k.shape[1]:
+        raise ValueError("k and v must have the same number of heads")
+    for (name, t), out in zip(given, outs):
+        if out is not None and (_need(out, torch.bfloat16, name + "_out").shape != t.shape or out.get_device() != dev):
+            raise ValueError(f"{name}_out must have shape {tuple(t.shape)} on {q.device}")
+    for name, t, dtype, n in (("positions", positions, torch.int32, q.shape[0]), ("inv_freq", inv_freq, torch.float32, -1),
+                              ("q_weight", weights[0], torch.float32, HEAD_DIM),
+                              ("k_weight", weights[1], torch.float32, HEAD_DIM)):
+        if t is None and name.endswith("weight"):
+            continue
+        if _need(t, dtype, name).get_device() != dev or t.dim() != 1:
+            raise ValueError(f"{name} must be one-dimensional on {q.device}")
+        if n >= 0 and t.shape[0] != n:
+            raise ValueError(f"{name} must have shape ({n},)")
+    raise ValueError("the tensors do not fit")
+
+
 def qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps: float = 1e-6, v=None,
                  interleaved: bool = False, norm: bool = True, rope_scale: float = 1.0, q_out=None, k_out=None,
                  v_out=None, stream=None):
@@ -565,57 +598,52 @@ def qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps: f
     rows on 16-byte boundaries); positions int32 [T] (negative: a padding row, left as it is); inv_freq fp32
     [rot_dim/2]; weights fp32 [128].  Returns contiguous bf16 (q, k), or (q, k, v) when v is given."""
     torch = _t()
-    bf16, dt, dev = torch.bfloat16, q.dtype, q.get_device()
-    kind = 0 if dt is bf16 else 1 if dt is torch.float16 else 2 if dt is torch.float32 else -1
-    if kind < 0:
-        raise TypeError(f"q must be bfloat16, float16 or float32, got {dt}")
-    for name, t in (("k", k), ("v", v)):
-        if t is not None and t.dtype is not dt:
-            raise TypeError(f"{name} must be {dt} like q, got {t.dtype}")
-
-    def view(t, name):  # rows of 128, heads and tokens at any stride
-        shape, st = t.shape, t.stride()
-        if dev < 0 or t.get_device() != dev:
-            raise ValueError(f"{name} must be a CUDA tensor on one device with q")
-        if len(shape) != 3 or shape[2] != HEAD_DIM or st[2] != 1 or shape[0] != tokens:
-            raise ValueError(f"{name} must be [T][heads][{HEAD_DIM}] with contiguous rows, got {tuple(shape)}")
-        # the stride of a dimension of one is never used, whatever it says
-        return shape, (st[0] if tokens > 1 else 0, st[1] if shape[1] > 1 else 0)
-
-    def result(t, shape, name):
-        if t is None:
-            return torch.empty(shape, dtype=bf16, device=q.device)
-        if t.dtype is not bf16 or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
-            _need(t, bf16, name)
-            raise ValueError(f"{name} must have shape {tuple(shape)} on {q.device}")
-        return t
-
-    def small(t, want, name, n):
-        if t is None or t.dtype is not want or t.get_device() != dev or not t.is_contiguous() or t.dim() != 1:
-            _need(t, want, name)
-            raise ValueError(f"{name} must be one-dimensional on {q.device}")
-        if n >= 0 and t.shape[0] != n:
-            raise ValueError(f"{name} must have shape ({n},)")
-        return t.data_ptr()
-
-    tokens = q.shape[0] if q.dim() else -1
-    (qs, qst), (ks, kst) = view(q, "q"), view(k, "k")
-    q_out, k_out = result(q_out, qs, "q_out"), result(k_out, ks, "k_out")
-    if v is not None:
-        vs, (vt, vh) = view(v, "v")
-        if vs[1] != ks[1]:
-            raise ValueError("k and v must have the same number of heads")
-        v_out = result(v_out, vs, "v_out")
-        vp, vo = v.data_ptr(), v_out.data_ptr()
-    else:
+    bf16, f32, dt, dev = torch.bfloat16, torch.float32, q.dtype, q.get_device()
+    kind = 0 if dt is bf16 else 1 if dt is torch.float16 else 2 if dt is f32 else -1
+    fits = (kind >= 0 and dev >= 0 and k.dtype is dt and k.get_device() == dev and q.dim() == 3 and k.dim() == 3
+            and positions is not None and inv_freq is not None)
+    if fits:
+        (tokens, hq, d), (qt, qh, q1) = q.shape, q.stride()
+        (kt_, hkv, kd), (kt, kh, k1) = k.shape, k.stride()
+        fits = d == HEAD_DIM and kd == HEAD_DIM and q1 == 1 and k1 == 1 and kt_ == tokens
+    if fits and v is not None:
+        fits = v.dtype is dt and v.get_device() == dev and v.shape == k.shape
+        if fits:
+            vt, vh, v1 = v.stride()
+            fits = v1 == 1
+    if fits:
+        for t, x in ((q_out, q), (k_out, k), (v_out, v)):
+            if t is not None and x is not None and not (t.dtype is bf16 and t.shape == x.shape and t.is_contiguous()
+                                                        and t.get_device() == dev):
+                fits = False
+        fits = (fits and positions.dtype is torch.int32 and positions.shape == (tokens,) and positions.is_contiguous()
+                and positions.get_device() == dev and inv_freq.dtype is f32 and inv_freq.dim() == 1
+                and inv_freq.is_contiguous() and inv_freq.get_device() == dev)
+        for t in (q_weight, k_weight):
+            if t is not None and not (t.dtype is f32 and t.shape == _WEIGHT and t.is_contiguous() and t.get_device() == dev):
+                fits = False
+    if not fits:
+        _rope_refuse(q, k, v, positions, inv_freq, (q_weight, k_weight), (q_out, k_out, v_out))
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=bf16, device=q.device)
+    if k_out is None:
+        k_out = torch.empty(k.shape, dtype=bf16, device=q.device)
+    if v is None:
         vp = vo = vt = vh = 0
-    f32 = torch.float32
-    a = _ROPE.pack(tokens, qs[1], ks[1], HEAD_DIM, kind, 0 if inv_freq is None else 2 * inv_freq.numel(),
-                   bool(interleaved), bool(norm), eps, rope_scale, q.data_ptr(), k.data_ptr(), vp, qst[0], qst[1],
-                   kst[0], kst[1], vt, vh, small(positions, torch.int32, "positions", tokens),
-                   small(inv_freq, f32, "inv_freq", -1), 0 if q_weight is None else small(q_weight, f32, "q_weight", HEAD_DIM),
-                   0 if k_weight is None else small(k_weight, f32, "k_weight", HEAD_DIM), q_out.data_ptr(),
-                   k_out.data_ptr(), vo)
+    else:
+        if v_out is None:
+            v_out = torch.empty(v.shape, dtype=bf16, device=q.device)
+        vp, vo = v.data_ptr(), v_out.data_ptr()
+    if tokens == 1:  # the stride of a dimension of one is never used, whatever it says
+        qt = kt = vt = 0
+    if hq == 1:
+        qh = 0
+    if hkv == 1:
+        kh = vh = 0
+    a = _ROPE.pack(tokens, hq, hkv, HEAD_DIM, kind, 2 * inv_freq.shape[0], bool(interleaved), bool(norm), eps, rope_scale,
+                   q.data_ptr(), k.data_ptr(), vp, qt, qh, kt, kh, vt, vh, positions.data_ptr(), inv_freq.data_ptr(),
+                   0 if q_weight is None else q_weight.data_ptr(), 0 if k_weight is None else k_weight.data_ptr(),
+                   q_out.data_ptr(), k_out.data_ptr(), vo)
     _run(q, stream, lib().okv_qk_norm_rope, a)
     return (q_out, k_out) if v is None else (q_out, k_out, v_out)
 
