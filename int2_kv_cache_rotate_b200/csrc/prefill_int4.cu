@@ -224,7 +224,10 @@ __global__ void __launch_bounds__(kP4Threads, 1)
             const float bm = fmaxf(mx[0], mx[1]) * sc;
             const bool need = bm > m_use + kP4Slack;
             if (__any_sync(0xffffffffu, need)) {
-              // O_t holds every earlier chunk (S_t of this one was issued after its MMAs were done)
+              // O_t holds every earlier chunk (S_t of this one was issued after its MMAs were done).
+              // The weights read back below are this thread's own stores of the batches before:
+              // a load from TMEM is ordered behind them by this wait alone.
+              if (b > 0) um_wait_st();
               const float alpha = need ? p4_ex2(m_use - bm) : 1.f;  // 0 while the row has seen nothing
               if (i > 0) {
 #pragma unroll 1
