@@ -247,6 +247,8 @@ size_t okv_sink_bytes(int32_t num_seq_slots, int32_t num_kv_heads, int32_t num_s
  *   rotated_out: device fp32 [T][2][Hkv][d] (nullable), the rotated fp32
  *   vectors the quantiser saw.
  * Tokens with equal (slot, pos) in one call race; T = 0 is a no-op.
+ * A vector that is not finite after the rotation is stored as finite bytes that
+ * stand for no particular values.
  * Pages: gen-hub.ru "Что придумали в Together AI" (U, then H, then P_br);
  * bigsaas.top "Resultados e Métricas de Desempenho" (INT2). */
 okv_status okv_append_quantize(const okv_cache_desc* desc, const void* k, const void* v, int32_t T,
@@ -274,7 +276,8 @@ size_t okv_decode_workspace_bytes(const okv_cache_desc* desc, int32_t B);
  * S = num_sink, positions [0, min(S, L)) are read from the fp16 sink rows,
  * [S, L-W) from the INT2 blocks and [max(S, L-W), L) from the fp16 window;
  * q~ = q R_K, softmax(q~ x^T / sqrt(d)) over those, then o = o~ R_V^T.
- * L = 0 gives zeros.  Launches three kernels on `stream` (query rotation,
+ * L = 0 gives zeros; a query row that holds an infinity or a NaN gives NaN in
+ * its own output row (here and in the prefill).  Launches three kernels on `stream` (query rotation,
  * split-K attention, split combine with the value un-rotation).
  * Pages: aiforradalom.hu intro (decode streams the cache from HBM);
  * gen-hub.ru "Что придумали в Together AI" (rotations of Q and of SV). */

@@ -383,13 +383,11 @@ __global__ void __launch_bounds__(kDecWarps * 32) decode_simt_kernel(DecodeArgs 
         float mx = -INFINITY;
         for (int w = 0; w < kDecWarps; ++w) mx = fmaxf(mx, ml[(w * G + gg) * 2]);
         float o = 0.f, l = 0.f;
-        if (mx != -INFINITY) {
-          for (int w = 0; w < kDecWarps; ++w) {
-            const float mw = ml[(w * G + gg) * 2];
-            const float sc = (mw == -INFINITY) ? 0.f : exp2f(mw - mx);
-            o = fmaf(mo[(w * G + gg) * kD + ch], sc, o);
-            l = fmaf(ml[(w * G + gg) * 2 + 1], sc, l);
-          }
+        for (int w = 0; w < kDecWarps; ++w) {
+          const float mw = ml[(w * G + gg) * 2], lw = ml[(w * G + gg) * 2 + 1];
+          const float sc = lw == 0.f ? 0.f : exp2f(mw - mx);  // (a sum that is NaN goes on to the output)
+          o = fmaf(mo[(w * G + gg) * kD + ch], sc, o);
+          l = fmaf(lw, sc, l);
         }
         dst[gg * kPartStride + ch] = o;
         if (ch == 0) {
@@ -482,10 +480,11 @@ __global__ void __launch_bounds__(kCombThreads) combine_kernel(DecodeArgs a) {
   for (int w = 1; w < kCombWarps; ++w) mx = fmaxf(mx, redm[w]);
   float l = 0.f;
   for (int c = tid; c < ns; c += kCombThreads) {
-    const float m = ml[c];
-    const float w = (mx == -INFINITY || m == -INFINITY) ? 0.f : exp2f(m - mx);
+    // a split without a key has sum 0 and maximum -inf; a sum that is NaN (a
+    // query or a token that is not finite) goes on to the output
+    const float lc = wsum[c], w = lc == 0.f ? 0.f : exp2f(ml[c] - mx);
     ml[c] = w;
-    l = fmaf(wsum[c], w, l);
+    l = fmaf(lc, w, l);
   }
   l = warp_sum(l);
   if (lane == 0) redl[warp] = l;
@@ -493,7 +492,7 @@ __global__ void __launch_bounds__(kCombThreads) combine_kernel(DecodeArgs a) {
   l = 0.f;
 #pragma unroll
   for (int w = 0; w < kCombWarps; ++w) l += redl[w];
-  const float inv_l = l > 0.f ? 1.f / l : 0.f;
+  const float inv_l = l == 0.f ? 0.f : 1.f / l;
   // weighted sum of the splits
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll

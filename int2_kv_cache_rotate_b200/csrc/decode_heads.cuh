@@ -1653,15 +1653,13 @@ __global__ void __launch_bounds__(kHW * 32, (G <= 4) ? 2 : 1) decode_heads_kerne
         float mx = -INFINITY;
         for (int k = 0; k < wph; ++k) mx = fmaxf(mx, ml[((hh + k * hkv) * G + gg) * 2]);
         float o = 0.f, l = 0.f;
-        if (mx != -INFINITY) {
-          for (int k = 0; k < wph; ++k) {
-            const int w = hh + k * hkv;
-            const float mw = ml[(w * G + gg) * 2];
-            if (mw == -INFINITY) continue;
-            const float sc = exp2f(mw - mx);
-            o = fmaf(mo[((size_t)w * G + gg) * kD + ch], sc, o);
-            l = fmaf(ml[(w * G + gg) * 2 + 1], sc, l);
-          }
+        for (int k = 0; k < wph; ++k) {
+          const int w = hh + k * hkv;
+          const float mw = ml[(w * G + gg) * 2], lw = ml[(w * G + gg) * 2 + 1];
+          if (lw == 0.f) continue;  // a warp that saw no key (a sum that is NaN goes on to the output)
+          const float sc = exp2f(mw - mx);
+          o = fmaf(mo[((size_t)w * G + gg) * kD + ch], sc, o);
+          l = fmaf(lw, sc, l);
         }
         float* dst = a.part + ((size_t)(crange() + b) * a.hq + (size_t)qhead0(hh) + gg) * kPartStride;
         dst[ch] = o;

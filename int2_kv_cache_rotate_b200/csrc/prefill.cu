@@ -1128,8 +1128,9 @@ __global__ void __launch_bounds__(256) prefill_unrotate_kernel(const __grid_cons
     }
 #pragma unroll
     for (int k = 0; k < RW; ++k) {
-      const float top = warp_max(lr[k] > 0.f ? w[k] : -INFINITY);
-      w[k] = lr[k] > 0.f ? exp2f(w[k] - top) : 0.f;
+      // (a piece without a key has l = 0; an l that is NaN goes on to the output)
+      const float top = warp_max(lr[k] != 0.f ? w[k] : -INFINITY);
+      w[k] = lr[k] != 0.f ? exp2f(w[k] - top) : 0.f;
       lr[k] = warp_sum(w[k] * lr[k]);
     }
     // piece by piece, the warp's rows' loads in flight together (a row at
@@ -1156,7 +1157,7 @@ __global__ void __launch_bounds__(256) prefill_unrotate_kernel(const __grid_cons
   }
 #pragma unroll
   for (int k = 0; k < RW; ++k) {
-    const float inv = lr[k] > 0.f ? 1.f / lr[k] : 0.f;
+    const float inv = lr[k] == 0.f ? 0.f : 1.f / lr[k];
     // lane l: pre-permutation channels l + 32 aa = rotated channels 4 rev5(l) + rev2(aa)
     float y[4] = {o4[k].x * inv, o4[k].z * inv, o4[k].y * inv, o4[k].w * inv};
     wht128_warp(y, lane);

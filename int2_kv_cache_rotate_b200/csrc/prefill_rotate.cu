@@ -228,8 +228,9 @@ __global__ void __launch_bounds__(256, 2)
       }
 #pragma unroll
       for (int k = 0; k < kRoBatch; ++k) {
-        const float top = warp_max(l[k] > 0.f ? w[k] : -INFINITY);
-        w[k] = l[k] > 0.f ? exp2f(w[k] - top) : 0.f;
+        // (a piece without a key has l = 0; an l that is NaN goes on to the output)
+        const float top = warp_max(l[k] != 0.f ? w[k] : -INFINITY);
+        w[k] = l[k] != 0.f ? exp2f(w[k] - top) : 0.f;
         l[k] = warp_sum(w[k] * l[k]);
       }
 #pragma unroll 2
@@ -256,7 +257,7 @@ __global__ void __launch_bounds__(256, 2)
     }
 #pragma unroll
     for (int k = 0; k < kRoBatch; ++k) {
-      const float inv = l[k] > 0.f ? 1.f / l[k] : 0.f;
+      const float inv = l[k] == 0.f ? 0.f : 1.f / l[k];
       // lane l: pre-permutation channels l + 32 aa = rotated channels 4 rev5(l) + rev2(aa)
       float y[4] = {o4[k].x * inv, o4[k].z * inv, o4[k].y * inv, o4[k].w * inv};
       wht128_warp(y, lane);
