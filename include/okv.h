@@ -268,7 +268,7 @@ size_t okv_decode_workspace_bytes(const okv_cache_desc* desc, int32_t B);
 
 /* Decode attention for one new query per sequence.
  *   q: device bf16 [B][Hq][d]; seq_slot: device int32 [B] (row of block table
- *   and window ring); block_table as above; context_lens: device int32 [B],
+ *   and window ring; not looked at where the length is 0); block_table as above; context_lens: device int32 [B],
  *   tokens in the cache for each sequence (the caller appends the step's own
  *   token first); out: device fp32 [B][Hq][d]; workspace: device, at least
  *   okv_decode_workspace_bytes(desc, B) bytes, 256-B aligned.
@@ -384,7 +384,15 @@ okv_status okv_dequantize(const okv_cache_desc* desc, int32_t B, const int32_t* 
  *     other columns stay as they are;
  *   - its tokens take the next `new` rows of tok_slot and tok_pos:
  *     (slot, old), (slot, old + 1), ...; cu_tokens[b] is its first row;
- *   - context_lens[b] = slot_lens[slot] = old + new.
+ *   - context_lens[b] = slot_lens[slot] = old + new; tok_lens holds it in the
+ *     row of the request's last token, and 0 in every other row.
+ * The queries of a step lie by token row, so okv_decode_step and
+ * okv_decode_attention take seq_slot = tok_slot, context_lens = tok_lens and
+ * B = the rows: row i of q and out is then token row i, whatever requests are
+ * padding, dropped or without a new token, and rows of length 0 (padding, and
+ * all but the last token of a request that gains several: those are
+ * okv_prefill_attention's) give zeros.  (The plan's own seq_slot and
+ * context_lens go with queries gathered to one row per request.)
  * cu_tokens[num_requests] is the number of rows used, *free_count_out = count
  * minus the blocks taken; rows behind the last token get slot = position = -1
  * (padding rows: see OKV_PAD_ROWS).  The first request that the free list or
@@ -426,6 +434,7 @@ typedef struct {
   int32_t* tok_pos;            /* device [max_tokens], out                 */
   int32_t* free_count_out;     /* device [1], out                          */
   uint32_t* status_word;       /* device, nullable: OKV_DEV_* flags (OR-ed) */
+  int32_t* tok_lens;           /* device [max_tokens], nullable, out       */
 } okv_plan;
 size_t okv_plan_workspace_bytes(int32_t num_requests);
 okv_status okv_plan_append(const okv_plan* plan, void* workspace, size_t workspace_bytes, void* stream);

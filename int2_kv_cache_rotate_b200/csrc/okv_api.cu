@@ -127,7 +127,7 @@ using namespace okv;
 
 extern "C" {
 
-int32_t okv_version(void) { return 4; }
+int32_t okv_version(void) { return 5; }
 
 okv_status okv_time_next_decode_kernel(void* start_event, void* stop_event) {
   if ((start_event == nullptr) != (stop_event == nullptr))

@@ -8,7 +8,9 @@
 // NT_{b-1} .. NT_b - 1 and its new table columns the pool's blocks
 // count - 1 - NB_{b-1}, downwards.  A new column c has exactly one new token
 // at position 16 c, so the thread that writes that token's row also writes
-// the column: one pass over token rows does everything but the scan.
+// the column: one pass over token rows does everything but the scan.  The row
+// of a request's last new token also gets the request's length, every other row
+// 0: with them a decode call takes token rows as its entries.
 //
 // Bound: the scan is latency (a few loads and a block-wide scan), the rows are
 // 8 bytes written per token.
@@ -69,11 +71,13 @@ static_assert(kPlWarps == 32, "scan2 lets one warp hold every warp's total");
 // Row `row` of the token maps: its request is the one with cu[b] <= row <
 // cu[b + 1] (n_req requests, cu[n_req] = total); `old_of` and `off_of` give a
 // request's tokens before this step and its first block's distance from the
-// pool's end.
+// pool's end.  len: the request's tokens after the step in the row of its last
+// new token, else 0.
 template <typename Cu, typename Slot, typename Old, typename Off>
 __device__ __forceinline__ void plan_row(const okv_plan& p, int row, int lo, int hi, int total, int count, const Cu& cu,
-                                         const Slot& slot_of, const Old& old_of, const Off& off_of, int& slot, int& pos) {
+                                         const Slot& slot_of, const Old& old_of, const Off& off_of, int& slot, int& pos, int& len) {
   slot = pos = -1;
+  len = 0;
   if (row >= total) return;
   while (lo < hi) {  // the last request whose first row is <= row
     const int mid = (lo + hi + 1) >> 1;
@@ -83,6 +87,7 @@ __device__ __forceinline__ void plan_row(const okv_plan& p, int row, int lo, int
   slot = slot_of(lo);
   const int old = old_of(lo);
   pos = old + row - cu(lo);
+  len = row + 1 == cu(lo + 1) ? pos + 1 : 0;
   if ((pos & (kBlock - 1)) == 0) {
     const int col = pos >> 4, first = (old + kBlock - 1) >> 4;
     p.block_table[(size_t)slot * p.max_blocks_per_seq + col] = p.free_blocks[count - 1 - off_of(lo) - (col - first)];
@@ -195,11 +200,12 @@ __global__ void __launch_bounds__(kPlThreads) plan_scan_kernel(PlanArgs a) {
     if (tid == 0) s_cu[B] = total_rows;
     __syncthreads();
     for (int row = tid; row < p.max_tokens; row += kPlThreads) {
-      int slot, pos;
+      int slot, pos, len;
       plan_row(p, row, 0, B - 1, total_rows, count, [&](int i) { return s_cu[i]; }, [&](int i) { return s_slot[i]; },
-               [&](int i) { return s_old[i]; }, [&](int i) { return s_off[i]; }, slot, pos);
+               [&](int i) { return s_old[i]; }, [&](int i) { return s_off[i]; }, slot, pos, len);
       p.tok_slot[row] = slot;
       p.tok_pos[row] = pos;
+      if (p.tok_lens != nullptr) p.tok_lens[row] = len;
     }
   }
 }
@@ -220,7 +226,7 @@ __global__ void __launch_bounds__(kPlFillThreads) plan_fill_kernel(PlanArgs a) {
     if (p.cu_tokens[mid] <= r0) lo = mid;
     else hi = mid - 1;
   }
-  int slot[kPlRows], pos[kPlRows];
+  int slot[kPlRows], pos[kPlRows], len[kPlRows];
 #pragma unroll
   for (int i = 0; i < kPlRows; ++i) {
     const int row = (int)r0 + i;
@@ -229,17 +235,22 @@ __global__ void __launch_bounds__(kPlFillThreads) plan_fill_kernel(PlanArgs a) {
     if (row < total)
       while (lo + 1 < B && p.cu_tokens[lo + 1] <= row) ++lo;
     plan_row(p, row, lo, lo, total, count, [&](int b) { return p.cu_tokens[b]; }, [&](int b) { return p.seq_slot[b]; },
-             [&](int b) { return a.old_len[b]; }, [&](int b) { return a.blk_off[b]; }, slot[i], pos[i]);
+             [&](int b) { return a.old_len[b]; }, [&](int b) { return a.blk_off[b]; }, slot[i], pos[i],
+             len[i]);
   }
-  if (r0 + kPlRows <= p.max_tokens && ((((uintptr_t)p.tok_slot | (uintptr_t)p.tok_pos) & 15u) == 0)) {
+  const bool lens = p.tok_lens != nullptr;
+  if (r0 + kPlRows <= p.max_tokens &&
+      ((((uintptr_t)p.tok_slot | (uintptr_t)p.tok_pos | (uintptr_t)p.tok_lens) & 15u) == 0)) {
     *reinterpret_cast<int4*>(p.tok_slot + r0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
     *reinterpret_cast<int4*>(p.tok_pos + r0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+    if (lens) *reinterpret_cast<int4*>(p.tok_lens + r0) = make_int4(len[0], len[1], len[2], len[3]);
   } else {
 #pragma unroll
     for (int i = 0; i < kPlRows; ++i)
       if (r0 + i < p.max_tokens) {
         p.tok_slot[r0 + i] = slot[i];
         p.tok_pos[r0 + i] = pos[i];
+        if (lens) p.tok_lens[r0 + i] = len[i];
       }
   }
 }
@@ -290,7 +301,7 @@ okv_status okv_plan_append(const okv_plan* plan, void* workspace, size_t workspa
                         (const void*)p.free_blocks, (const void*)p.free_count, (const void*)p.block_table,
                         (const void*)p.slot_lens, (const void*)p.context_lens, (const void*)p.cu_tokens,
                         (const void*)p.tok_slot, (const void*)p.tok_pos, (const void*)p.free_count_out,
-                        (const void*)p.status_word})
+                        (const void*)p.status_word, (const void*)p.tok_lens})
     if ((uintptr_t)x % 4) return fail(OKV_ERR_INVALID_ARG, "every array must be 4-byte aligned");
   const cudaStream_t s = (cudaStream_t)stream;
   const size_t bitmap = (size_t)2 * ((p.num_seq_slots + 31) / 32) * sizeof(uint32_t);

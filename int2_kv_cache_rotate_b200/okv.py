@@ -61,7 +61,7 @@ class PlanArgs(ctypes.Structure):
                                               "num_free")] + \
                [(n, ctypes.c_void_p) for n in ("seq_slot", "cached_lens", "new_lens", "free_blocks", "free_count",
                                                "block_table", "slot_lens", "context_lens", "cu_tokens", "tok_slot",
-                                               "tok_pos", "free_count_out", "status_word")]
+                                               "tok_pos", "free_count_out", "status_word", "tok_lens")]
 
 
 class NormRopeArgs(ctypes.Structure):
@@ -76,7 +76,7 @@ class NormRopeArgs(ctypes.Structure):
 
 
 # the same two structures as bytes, for calls that fill every field at once
-_PLAN, _ROPE = struct.Struct("5i4x13P"), struct.Struct("8i2f3P6q7P")
+_PLAN, _ROPE = struct.Struct("5i4x14P"), struct.Struct("8i2f3P6q7P")
 _WEIGHT = (HEAD_DIM,)
 assert _PLAN.size == ctypes.sizeof(PlanArgs) and _ROPE.size == ctypes.sizeof(NormRopeArgs)
 
@@ -500,6 +500,8 @@ class AppendPlan:
     outputs that the step's other calls take:
 
       tok_slot, tok_pos  int32 [max_tokens]: sequence slot and position of every new token, -1 behind the last
+      tok_lens           int32 [max_tokens]: tokens of the request after the step in the row of its last new token,
+                         0 in every other row: with tok_slot, what a decode call over the token rows takes
       context_lens       int32 [batch]: tokens of every request after the step
       cu_tokens          int32 [batch + 1]: first token row of every request
       free_count         int32 [1]: blocks left in the pool
@@ -515,6 +517,7 @@ class AppendPlan:
         i32 = dict(dtype=torch.int32, device=device)
         self.tok_slot = torch.full((max_tokens,), -1, **i32)
         self.tok_pos = torch.full((max_tokens,), -1, **i32)
+        self.tok_lens = torch.zeros(max_tokens, **i32)
         self.context_lens = torch.zeros(batch, **i32)
         self.cu_tokens = torch.zeros(batch + 1, **i32)
         self.free_count = torch.zeros(1, **i32)
@@ -522,7 +525,7 @@ class AppendPlan:
         self.ws = torch.empty(int(lib().okv_plan_workspace_bytes(batch)), dtype=torch.uint8, device=device)
         self._fn, self._dev = lib().okv_plan_append, self.tok_slot.get_device()
         self._outs = tuple(t.data_ptr() for t in (self.context_lens, self.cu_tokens, self.tok_slot, self.tok_pos,
-                                                  self.free_count, self.status))
+                                                  self.free_count, self.status, self.tok_lens))
         self._ws = (self.ws.data_ptr(), self.ws.numel())
 
     def build(self, seq_slot, cached_lens, new_lens, block_table, slot_lens, free_blocks, free_count, stream=None):
