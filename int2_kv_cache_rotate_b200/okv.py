@@ -216,10 +216,27 @@ def _ints(t, name, least):
     raise ValueError(f"{name} must hold at least {least} values, got {t.numel()}")
 
 
-def _out(cache, out, rows, device):
+def _new(shape, dtype, device, stream):
+    """A tensor that a call makes for itself and writes on `stream`: from that stream's pool, so that nothing queued on
+    another stream still uses its memory, and kept from reuse until the caller's current stream is past it."""
+    torch = _t()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(t.device))
+    return t
+
+
+def _scratch(nbytes, device, stream):
+    """A workspace that a call makes for itself."""
+    return _new(max(nbytes, 256), _t().uint8, device, stream)
+
+
+def _out(cache, out, rows, device, stream):
     """The output of `rows` query rows (a new fp32 tensor when None) and the descriptor that writes its type."""
     if out is None:
-        return _torch.empty((rows, cache.hq, HEAD_DIM), dtype=_torch.float32, device=device), cache.desc
+        return _new((rows, cache.hq, HEAD_DIM), _torch.float32, device, stream), cache.desc
     desc = _desc_for(cache, out)
     if out.numel() < rows * cache.hq * HEAD_DIM:
         raise ValueError(f"out must hold [{rows}][{cache.hq}][{HEAD_DIM}] values, got {tuple(out.shape)}")
@@ -354,13 +371,6 @@ def decode_workspace_bytes(cache: Cache, batch: int) -> int:
     return int(lib().okv_decode_workspace_bytes(ctypes.byref(cache.desc), batch))
 
 
-def _scratch(t, stream):
-    """A workspace that a call makes for itself: its memory is not handed out again before `stream` is past the call."""
-    if stream is not None:
-        t.record_stream(stream)
-    return t
-
-
 def workspace(cache: Cache, batch: int):
     return _t().empty(max(decode_workspace_bytes(cache, batch), 256), dtype=_torch.uint8, device=cache.pages.device)
 
@@ -384,9 +394,9 @@ def decode_attention(cache: Cache, q, seq_slot, block_table, context_lens, out=N
     """Decode attention of one query per sequence; out: fp32 (a new tensor when None) or bf16 [B, Hq, 128]."""
     _need(q, _t().bfloat16, "q")
     B, seq, table, ctx = _decode_args(cache, q, seq_slot, block_table, context_lens)
-    out, desc = _out(cache, out, B, q.device)
+    out, desc = _out(cache, out, B, q.device, stream)
     if ws is None:
-        ws = _scratch(workspace(cache, B), stream)
+        ws = _scratch(decode_workspace_bytes(cache, B), q.device, stream)
     _run(q, stream, lib().okv_decode_attention, ctypes.byref(desc), q.data_ptr(), B, seq, table, ctx, out.data_ptr(),
          ws.data_ptr(), ws.numel())
     return out
@@ -405,9 +415,9 @@ def _step_args(cache, k, v, new_seq_slot, new_pos, slot_lens, q, seq_slot, block
     slots = cache.num_seq_slots if T else 0
     if T and not B:
         _ints(block_table, "block_table", slots * cache.max_blocks_per_seq)
-    out, desc = _out(cache, out, B, q.device)
+    out, desc = _out(cache, out, B, q.device, stream)
     if ws is None:
-        ws = _scratch(workspace(cache, B), stream)
+        ws = _scratch(decode_workspace_bytes(cache, B), q.device, stream)
     args = (ctypes.byref(desc), k.data_ptr(), v.data_ptr(), T, _least(new_seq_slot, "new_seq_slot", T),
             _least(new_pos, "new_pos", T), _least(slot_lens, "slot_lens", slots), q.data_ptr(), B, seq, table, ctx,
             out.data_ptr(), ws.data_ptr(), ws.numel())
@@ -469,7 +479,7 @@ def decode_attention_noalloc(cache: Cache, q, seq_slot, block_table, context_len
     """Decode attention with the library's static scratch (no workspace, no allocation in the library)."""
     _need(q, _t().bfloat16, "q")
     B, seq, table, ctx = _decode_args(cache, q, seq_slot, block_table, context_lens)
-    out, desc = _out(cache, out, B, q.device)
+    out, desc = _out(cache, out, B, q.device, stream)
     _run(q, stream, lib().okv_decode_attention_noalloc, ctypes.byref(desc), q.data_ptr(), B, seq, table, ctx,
          out.data_ptr())
     return out
@@ -485,10 +495,9 @@ def prefill_attention(cache: Cache, q, slot: int, context_len: int, block_table,
     when out is None) or in out's type, fp32 or bf16."""
     T = _heads(q, _t().bfloat16, "q", cache.hq)
     table = _ints(block_table, "block_table", cache.num_seq_slots * cache.max_blocks_per_seq if T else 0)
-    out, desc = _out(cache, out, T, q.device)
+    out, desc = _out(cache, out, T, q.device, stream)
     if ws is None:
-        ws = _scratch(_torch.empty(max(prefill_workspace_bytes(cache, T), 256), dtype=_torch.uint8, device=q.device),
-                      stream)
+        ws = _scratch(prefill_workspace_bytes(cache, T), q.device, stream)
     _run(q, stream, lib().okv_prefill_attention, ctypes.byref(desc), q.data_ptr(), T, int(slot), int(context_len),
          table, out.data_ptr(), ws.data_ptr(), ws.numel())
     return out
@@ -628,14 +637,14 @@ def qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps: f
     if not fits:
         _rope_refuse(q, k, v, positions, inv_freq, (q_weight, k_weight), (q_out, k_out, v_out))
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=bf16, device=q.device)
+        q_out = _new(q.shape, bf16, q.device, stream)
     if k_out is None:
-        k_out = torch.empty(k.shape, dtype=bf16, device=q.device)
+        k_out = _new(k.shape, bf16, q.device, stream)
     if v is None:
         vp = vo = vt = vh = 0
     else:
         if v_out is None:
-            v_out = torch.empty(v.shape, dtype=bf16, device=q.device)
+            v_out = _new(v.shape, bf16, q.device, stream)
         vp, vo = v.data_ptr(), v_out.data_ptr()
     if tokens == 1:  # the stride of a dimension of one is never used, whatever it says
         qt = kt = vt = 0
@@ -666,7 +675,7 @@ def dequantize(cache: Cache, seq_slot, block_table, context_lens, max_ctx: int, 
         _need(t, torch.int32, name)
     batch = seq_slot.shape[0]
     if out is None:
-        out = torch.empty((batch, cache.hkv, max_ctx, HEAD_DIM), dtype=torch.float32, device=seq_slot.device)
+        out = _new((batch, cache.hkv, max_ctx, HEAD_DIM), torch.float32, seq_slot.device, stream)
     desc = _desc_for(cache, out)
     if out.numel() < batch * cache.hkv * max(max_ctx, 0) * HEAD_DIM:
         raise ValueError(f"out must hold [{batch}][{cache.hkv}][{max_ctx}][{HEAD_DIM}] values, got {tuple(out.shape)}")
