@@ -455,23 +455,22 @@ class DecodeStepCall:
         import torch
         if self._graph is not None:
             if self._stream is None:
-                self._graph.replay()
+                self._graph.replay()  # (on the current stream of the device it was recorded on)
             else:
                 with torch.cuda.stream(self._stream):
                     self._graph.replay()
             return self.out
-        status = self._fn(*self._args, _stream(self._stream))
-        if status != OK:
-            _check(status)
+        _run(self.out, self._stream, self._fn, *self._args)
         if self._want_graph:
-            # record the same call (the library allocates nothing and only launches)
-            cap = torch.cuda.Stream()
-            cap.wait_stream(torch.cuda.current_stream() if self._stream is None else self._stream)
-            g = torch.cuda.CUDAGraph()
-            with torch.cuda.graph(g, stream=cap):
-                status = self._fn(*self._args, cap.cuda_stream)
-            _check(status)
-            self._graph = g
+            with torch.cuda.device(self.out.device):
+                # record the same call (the library allocates nothing and only launches)
+                cap = torch.cuda.Stream()
+                cap.wait_stream(torch.cuda.current_stream() if self._stream is None else self._stream)
+                g = torch.cuda.CUDAGraph()
+                with torch.cuda.graph(g, stream=cap):
+                    status = self._fn(*self._args, cap.cuda_stream)
+                _check(status)
+                self._graph = g
         return self.out
 
 
