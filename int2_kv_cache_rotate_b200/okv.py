@@ -194,18 +194,17 @@ def _need(t, dtype, name, device=True):
 
 
 def _heads(t, dtype, name, heads):
-    """t: contiguous [rows][heads][128] on a GPU; returns its rows (none needs no shape)."""
+    """t: contiguous [rows][heads][128] on a GPU, in any dimensions behind the first; returns its rows."""
     return _rows(_need(t, dtype, name), name, heads)
 
 
 def _rows(t, name, heads):
     """The rows of a tensor that _need has passed."""
-    shape = t.shape
-    if len(shape) == 3 and shape[1] == heads and shape[2] == HEAD_DIM:
-        return shape[0]
-    if t.numel() == 0:
-        return 0
-    raise ValueError(f"{name} must be [rows][{heads}][{HEAD_DIM}], got {tuple(shape)}")
+    n = t.numel()
+    rows = n // (heads * HEAD_DIM)
+    if n == 0 or (t.shape and t.shape[0] == rows and n == rows * heads * HEAD_DIM):
+        return rows
+    raise ValueError(f"{name} must be [rows][{heads}][{HEAD_DIM}], got {tuple(t.shape)}")
 
 
 def _ints(t, name, least):
@@ -231,6 +230,19 @@ def _new(shape, dtype, device, stream):
 def _scratch(nbytes, device, stream):
     """A workspace that a call makes for itself."""
     return _new(max(nbytes, 256), _t().uint8, device, stream)
+
+
+def _for_slots(cache, desc, block_table, slot_lens=None):
+    """desc, or where the block table or slot_lens have fewer rows than the cache has sequence slots, a copy with as
+    many slots as they have: the kernels then skip and flag a slot beyond them like one beyond the cache's."""
+    slots = block_table.numel() // cache.max_blocks_per_seq
+    if slot_lens is not None:
+        slots = min(slots, slot_lens.numel())
+    if slots >= cache.num_seq_slots:
+        return desc
+    d = CacheDesc.from_buffer_copy(desc)
+    d.num_seq_slots = slots
+    return d
 
 
 def _out(cache, out, rows, device, stream):
@@ -360,11 +372,11 @@ def append_quantize(cache: Cache, k, v, seq_slot, pos, block_table, slot_lens, p
         _need(rotated_out, torch.float32, "rotated_out")
         if rotated_out.numel() < 2 * k.numel():
             raise ValueError("rotated_out must hold [T][2][Hkv][128] values")
-    slots = cache.num_seq_slots if T else 0
-    _run(k, stream, lib().okv_append_quantize, ctypes.byref(cache.desc), k.data_ptr(), v.data_ptr(), T,
-         _ints(seq_slot, "seq_slot", T), _ints(pos, "pos", T),
-         _ints(block_table, "block_table", slots * cache.max_blocks_per_seq), _ints(slot_lens, "slot_lens", slots),
-         PRE_ROTATED if pre_rotated else 0, _ptr(rotated_out))
+    args = (k.data_ptr(), v.data_ptr(), T, _ints(seq_slot, "seq_slot", T), _ints(pos, "pos", T),
+            _ints(block_table, "block_table", cache.max_blocks_per_seq if T else 0),
+            _ints(slot_lens, "slot_lens", 1 if T else 0), PRE_ROTATED if pre_rotated else 0, _ptr(rotated_out))
+    desc = _for_slots(cache, cache.desc, block_table, slot_lens) if T else cache.desc
+    _run(k, stream, lib().okv_append_quantize, ctypes.byref(desc), *args)
 
 
 def decode_workspace_bytes(cache: Cache, batch: int) -> int:
@@ -385,8 +397,8 @@ def _least(t, name, least):
 def _decode_args(cache, q, seq_slot, block_table, context_lens):
     """Rows of q (which _need has passed), and the pointers of a decode call's integer arrays."""
     B = _rows(q, "q", cache.hq)
-    slots = cache.num_seq_slots if B else 0
-    return (B, _ints(seq_slot, "seq_slot", B), _ints(block_table, "block_table", slots * cache.max_blocks_per_seq),
+    return (B, _ints(seq_slot, "seq_slot", B),
+            _ints(block_table, "block_table", cache.max_blocks_per_seq if B else 0),
             _ints(context_lens, "context_lens", B))
 
 
@@ -395,6 +407,8 @@ def decode_attention(cache: Cache, q, seq_slot, block_table, context_lens, out=N
     _need(q, _t().bfloat16, "q")
     B, seq, table, ctx = _decode_args(cache, q, seq_slot, block_table, context_lens)
     out, desc = _out(cache, out, B, q.device, stream)
+    if B:
+        desc = _for_slots(cache, desc, block_table)
     if ws is None:
         ws = _scratch(decode_workspace_bytes(cache, B), q.device, stream)
     _run(q, stream, lib().okv_decode_attention, ctypes.byref(desc), q.data_ptr(), B, seq, table, ctx, out.data_ptr(),
@@ -412,14 +426,15 @@ def _step_args(cache, k, v, new_seq_slot, new_pos, slot_lens, q, seq_slot, block
     T = _rows(k, "k", cache.hkv)
     if _rows(v, "v", cache.hkv) != T:
         raise ValueError("k and v must have the same number of rows")
-    slots = cache.num_seq_slots if T else 0
     if T and not B:
-        _ints(block_table, "block_table", slots * cache.max_blocks_per_seq)
+        _ints(block_table, "block_table", cache.max_blocks_per_seq)
     out, desc = _out(cache, out, B, q.device, stream)
+    if T or B:
+        desc = _for_slots(cache, desc, block_table, slot_lens if T else None)
     if ws is None:
         ws = _scratch(decode_workspace_bytes(cache, B), q.device, stream)
     args = (ctypes.byref(desc), k.data_ptr(), v.data_ptr(), T, _least(new_seq_slot, "new_seq_slot", T),
-            _least(new_pos, "new_pos", T), _least(slot_lens, "slot_lens", slots), q.data_ptr(), B, seq, table, ctx,
+            _least(new_pos, "new_pos", T), _least(slot_lens, "slot_lens", 1 if T else 0), q.data_ptr(), B, seq, table, ctx,
             out.data_ptr(), ws.data_ptr(), ws.numel())
     return out, args, (desc, ws)
 
@@ -479,6 +494,8 @@ def decode_attention_noalloc(cache: Cache, q, seq_slot, block_table, context_len
     _need(q, _t().bfloat16, "q")
     B, seq, table, ctx = _decode_args(cache, q, seq_slot, block_table, context_lens)
     out, desc = _out(cache, out, B, q.device, stream)
+    if B:
+        desc = _for_slots(cache, desc, block_table)
     _run(q, stream, lib().okv_decode_attention_noalloc, ctypes.byref(desc), q.data_ptr(), B, seq, table, ctx,
          out.data_ptr())
     return out
@@ -493,8 +510,10 @@ def prefill_attention(cache: Cache, q, slot: int, context_len: int, block_table,
     context_len - T .. context_len - 1 of sequence `slot`) over the cache; returns [T, Hq, 128] in fp32 (a new tensor
     when out is None) or in out's type, fp32 or bf16."""
     T = _heads(q, _t().bfloat16, "q", cache.hq)
-    table = _ints(block_table, "block_table", cache.num_seq_slots * cache.max_blocks_per_seq if T else 0)
+    table = _ints(block_table, "block_table", cache.max_blocks_per_seq if T else 0)
     out, desc = _out(cache, out, T, q.device, stream)
+    if T:
+        desc = _for_slots(cache, desc, block_table)
     if ws is None:
         ws = _scratch(prefill_workspace_bytes(cache, T), q.device, stream)
     _run(q, stream, lib().okv_prefill_attention, ctypes.byref(desc), q.data_ptr(), T, int(slot), int(context_len),
@@ -678,8 +697,9 @@ def dequantize(cache: Cache, seq_slot, block_table, context_lens, max_ctx: int, 
     desc = _desc_for(cache, out)
     if out.numel() < batch * cache.hkv * max(max_ctx, 0) * HEAD_DIM:
         raise ValueError(f"out must hold [{batch}][{cache.hkv}][{max_ctx}][{HEAD_DIM}] values, got {tuple(out.shape)}")
-    slots = cache.num_seq_slots if batch else 0
-    _run(out, stream, lib().okv_dequantize, ctypes.byref(desc), batch, seq_slot.data_ptr(),
-         _ints(block_table, "block_table", slots * cache.max_blocks_per_seq), _ints(context_lens, "context_lens", batch),
-         max_ctx, which, basis, source, out.data_ptr())
+    table = _ints(block_table, "block_table", cache.max_blocks_per_seq if batch else 0)
+    if batch:
+        desc = _for_slots(cache, desc, block_table)
+    _run(out, stream, lib().okv_dequantize, ctypes.byref(desc), batch, seq_slot.data_ptr(), table,
+         _ints(context_lens, "context_lens", batch), max_ctx, which, basis, source, out.data_ptr())
     return out
