@@ -179,23 +179,43 @@ def _run(t, stream, fn, *args):
         _check(status)
 
 
-def _need(t, dtype, name, device=True):
-    if t is not None and t.dtype is dtype and t.is_contiguous() and (t.is_cuda or not device):
-        return t
+def _need(t, dtype, name, dev=None):
+    """t: a contiguous tensor of that type on GPU `dev` (any GPU when None)."""
+    if t is not None and t.dtype is dtype and t.is_contiguous():
+        on = t.get_device()
+        if on >= 0 and (on == dev or dev is None):
+            return t
     if t is None:
         raise ValueError(f"{name} is required")
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if device and not t.is_cuda:
+    if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    return t
+    raise ValueError(f"{name} must be on the device of the call's other tensors, got {t.device}")
 
 
-def _heads(t, dtype, name, heads):
-    """t: contiguous [rows][heads][128] on a GPU, in any dimensions behind the first; returns its rows."""
-    return _rows(_need(t, dtype, name), name, heads)
+def _device(cache, t, name):
+    """The GPU of a call: that of its first tensor t, which the cache has to be on too."""
+    if t is None:
+        raise ValueError(f"{name} is required")
+    dev = t.get_device()
+    if dev >= 0 and cache is not None and dev != cache.dev:
+        raise ValueError(f"{name} must be on the cache's device, got {t.device}")
+    return dev
+
+
+def _ws(ws, dev):
+    """Address and bytes of a workspace that the caller gives."""
+    if ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError(f"ws must be contiguous on the device of the call's other tensors, got {ws.device}")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def _heads(t, dtype, name, heads, dev):
+    """t: contiguous [rows][heads][128] on GPU dev, in any dimensions behind the first; returns its rows."""
+    return _rows(_need(t, dtype, name, dev), name, heads)
 
 
 def _rows(t, name, heads):
@@ -207,11 +227,11 @@ def _rows(t, name, heads):
     raise ValueError(f"{name} must be [rows][{heads}][{HEAD_DIM}], got {tuple(t.shape)}")
 
 
-def _ints(t, name, least):
-    """t: contiguous int32 on a GPU with `least` values or more."""
-    if t is not None and t.dtype is _torch.int32 and t.is_cuda and t.is_contiguous() and t.numel() >= least:
+def _ints(t, name, least, dev):
+    """t: contiguous int32 on GPU dev with `least` values or more."""
+    if t is not None and t.dtype is _torch.int32 and t.get_device() == dev and t.is_contiguous() and t.numel() >= least:
         return t.data_ptr()
-    _need(t, _t().int32, name)
+    _need(t, _t().int32, name, dev)
     raise ValueError(f"{name} must hold at least {least} values, got {t.numel()}")
 
 
@@ -249,7 +269,7 @@ def _out(cache, out, rows, device, stream):
     """The output of `rows` query rows (a new fp32 tensor when None) and the descriptor that writes its type."""
     if out is None:
         return _new((rows, cache.hq, HEAD_DIM), _torch.float32, device, stream), cache.desc
-    desc = _desc_for(cache, out)
+    desc = _desc_for(cache, out, device.index)
     if out.numel() < rows * cache.hq * HEAD_DIM:
         raise ValueError(f"out must hold [{rows}][{cache.hq}][{HEAD_DIM}] values, got {tuple(out.shape)}")
     return out, desc
@@ -296,6 +316,7 @@ class Cache:
         self.u_k = torch.as_tensor(np.asarray(u_k, dtype=np.float32)).to(device).contiguous()
         self.u_v = torch.as_tensor(np.asarray(u_v, dtype=np.float32)).to(device).contiguous()
         self.status = torch.zeros(4, dtype=torch.int32, device=device)
+        self.dev = self.pages.get_device()
         # first num_sink positions of every sequence, fp16 (sink tokens)
         self.sink = torch.zeros((num_seq_slots, hkv, 2, max(num_sink, 0), HEAD_DIM), dtype=torch.float16,
                                 device=device)
@@ -321,13 +342,13 @@ class Cache:
         self.status.zero_()
 
 
-def _desc_for(cache: Cache, out):
+def _desc_for(cache: Cache, out, dev):
     """The cache's descriptor for a call that writes `out`: fp32, or bf16 (the OUT_BF16 format bit)."""
     torch = _t()
     if out.dtype is not torch.bfloat16:
-        _need(out, torch.float32, "out")
+        _need(out, torch.float32, "out", dev)
         return cache.desc
-    _need(out, torch.bfloat16, "out")
+    _need(out, torch.bfloat16, "out", dev)
     d = CacheDesc.from_buffer_copy(cache.desc)
     d.group |= OUT_BF16
     return d
@@ -365,16 +386,17 @@ def append_quantize(cache: Cache, k, v, seq_slot, pos, block_table, slot_lens, p
                     rotated_out=None, stream=None):
     torch = _t()
     dt = torch.float32 if pre_rotated else torch.bfloat16
-    T = _heads(k, dt, "k", cache.hkv)
-    if _heads(v, dt, "v", cache.hkv) != T:
+    dev = _device(cache, k, "k")
+    T = _heads(k, dt, "k", cache.hkv, dev)
+    if _heads(v, dt, "v", cache.hkv, dev) != T:
         raise ValueError("k and v must have the same number of rows")
     if rotated_out is not None:
-        _need(rotated_out, torch.float32, "rotated_out")
+        _need(rotated_out, torch.float32, "rotated_out", dev)
         if rotated_out.numel() < 2 * k.numel():
             raise ValueError("rotated_out must hold [T][2][Hkv][128] values")
-    args = (k.data_ptr(), v.data_ptr(), T, _ints(seq_slot, "seq_slot", T), _ints(pos, "pos", T),
-            _ints(block_table, "block_table", cache.max_blocks_per_seq if T else 0),
-            _ints(slot_lens, "slot_lens", 1 if T else 0), PRE_ROTATED if pre_rotated else 0, _ptr(rotated_out))
+    args = (k.data_ptr(), v.data_ptr(), T, _ints(seq_slot, "seq_slot", T, dev), _ints(pos, "pos", T, dev),
+            _ints(block_table, "block_table", cache.max_blocks_per_seq if T else 0, dev),
+            _ints(slot_lens, "slot_lens", 1 if T else 0, dev), PRE_ROTATED if pre_rotated else 0, _ptr(rotated_out))
     desc = _for_slots(cache, cache.desc, block_table, slot_lens) if T else cache.desc
     _run(k, stream, lib().okv_append_quantize, ctypes.byref(desc), *args)
 
@@ -394,40 +416,41 @@ def _least(t, name, least):
     return t.data_ptr()
 
 
-def _decode_args(cache, q, seq_slot, block_table, context_lens):
+def _decode_args(cache, q, seq_slot, block_table, context_lens, dev):
     """Rows of q (which _need has passed), and the pointers of a decode call's integer arrays."""
     B = _rows(q, "q", cache.hq)
-    return (B, _ints(seq_slot, "seq_slot", B),
-            _ints(block_table, "block_table", cache.max_blocks_per_seq if B else 0),
-            _ints(context_lens, "context_lens", B))
+    return (B, _ints(seq_slot, "seq_slot", B, dev),
+            _ints(block_table, "block_table", cache.max_blocks_per_seq if B else 0, dev),
+            _ints(context_lens, "context_lens", B, dev))
 
 
 def decode_attention(cache: Cache, q, seq_slot, block_table, context_lens, out=None, ws=None, stream=None):
     """Decode attention of one query per sequence; out: fp32 (a new tensor when None) or bf16 [B, Hq, 128]."""
-    _need(q, _t().bfloat16, "q")
-    B, seq, table, ctx = _decode_args(cache, q, seq_slot, block_table, context_lens)
+    dev = _device(cache, q, "q")
+    _need(q, _t().bfloat16, "q", dev)
+    B, seq, table, ctx = _decode_args(cache, q, seq_slot, block_table, context_lens, dev)
     out, desc = _out(cache, out, B, q.device, stream)
     if B:
         desc = _for_slots(cache, desc, block_table)
     if ws is None:
         ws = _scratch(decode_workspace_bytes(cache, B), q.device, stream)
     _run(q, stream, lib().okv_decode_attention, ctypes.byref(desc), q.data_ptr(), B, seq, table, ctx, out.data_ptr(),
-         ws.data_ptr(), ws.numel())
+         *_ws(ws, dev))
     return out
 
 
 def _step_args(cache, k, v, new_seq_slot, new_pos, slot_lens, q, seq_slot, block_table, context_lens, out, ws, stream):
     """Output, the library's arguments but for the stream, and what they point into."""
-    bf16 = _t().bfloat16
-    _need(k, bf16, "k"), _need(v, bf16, "v"), _need(q, bf16, "q")
+    bf16, dev = _t().bfloat16, _device(cache, q, "q")
+    _need(k, bf16, "k", dev), _need(v, bf16, "v", dev), _need(q, bf16, "q", dev)
     for name, t in (("new_seq_slot", new_seq_slot), ("new_pos", new_pos), ("slot_lens", slot_lens)):
-        _need(t, _torch.int32, name)
-    B, seq, table, ctx = _decode_args(cache, q, seq_slot, block_table, context_lens)
+        _need(t, _torch.int32, name, dev)
+    B, seq, table, ctx = _decode_args(cache, q, seq_slot, block_table, context_lens, dev)
     T = _rows(k, "k", cache.hkv)
     if _rows(v, "v", cache.hkv) != T:
         raise ValueError("k and v must have the same number of rows")
     if T and not B:
-        _ints(block_table, "block_table", cache.max_blocks_per_seq)
+        _ints(block_table, "block_table", cache.max_blocks_per_seq, dev)
     out, desc = _out(cache, out, B, q.device, stream)
     if T or B:
         desc = _for_slots(cache, desc, block_table, slot_lens if T else None)
@@ -435,7 +458,7 @@ def _step_args(cache, k, v, new_seq_slot, new_pos, slot_lens, q, seq_slot, block
         ws = _scratch(decode_workspace_bytes(cache, B), q.device, stream)
     args = (ctypes.byref(desc), k.data_ptr(), v.data_ptr(), T, _least(new_seq_slot, "new_seq_slot", T),
             _least(new_pos, "new_pos", T), _least(slot_lens, "slot_lens", 1 if T else 0), q.data_ptr(), B, seq, table, ctx,
-            out.data_ptr(), ws.data_ptr(), ws.numel())
+            out.data_ptr(), *_ws(ws, dev))
     return out, args, (desc, ws)
 
 
@@ -491,8 +514,9 @@ class DecodeStepCall:
 
 def decode_attention_noalloc(cache: Cache, q, seq_slot, block_table, context_lens, out=None, stream=None):
     """Decode attention with the library's static scratch (no workspace, no allocation in the library)."""
-    _need(q, _t().bfloat16, "q")
-    B, seq, table, ctx = _decode_args(cache, q, seq_slot, block_table, context_lens)
+    dev = _device(cache, q, "q")
+    _need(q, _t().bfloat16, "q", dev)
+    B, seq, table, ctx = _decode_args(cache, q, seq_slot, block_table, context_lens, dev)
     out, desc = _out(cache, out, B, q.device, stream)
     if B:
         desc = _for_slots(cache, desc, block_table)
@@ -509,15 +533,16 @@ def prefill_attention(cache: Cache, q, slot: int, context_len: int, block_table,
     """Causal attention of a prefill chunk (q: bf16 [T, Hq, 128], already appended at positions
     context_len - T .. context_len - 1 of sequence `slot`) over the cache; returns [T, Hq, 128] in fp32 (a new tensor
     when out is None) or in out's type, fp32 or bf16."""
-    T = _heads(q, _t().bfloat16, "q", cache.hq)
-    table = _ints(block_table, "block_table", cache.max_blocks_per_seq if T else 0)
+    dev = _device(cache, q, "q")
+    T = _heads(q, _t().bfloat16, "q", cache.hq, dev)
+    table = _ints(block_table, "block_table", cache.max_blocks_per_seq if T else 0, dev)
     out, desc = _out(cache, out, T, q.device, stream)
     if T:
         desc = _for_slots(cache, desc, block_table)
     if ws is None:
         ws = _scratch(prefill_workspace_bytes(cache, T), q.device, stream)
     _run(q, stream, lib().okv_prefill_attention, ctypes.byref(desc), q.data_ptr(), T, int(slot), int(context_len),
-         table, out.data_ptr(), ws.data_ptr(), ws.numel())
+         table, out.data_ptr(), *_ws(ws, dev))
     return out
 
 
@@ -688,18 +713,18 @@ def time_next_decode_kernel(start_event, stop_event):
 
 def dequantize(cache: Cache, seq_slot, block_table, context_lens, max_ctx: int, which: int, basis: int = 0,
                source: int = 0, out=None, stream=None):
-    torch = _t()
+    torch, dev = _t(), _device(cache, seq_slot, "seq_slot")
     for name, t in (("seq_slot", seq_slot), ("block_table", block_table), ("context_lens", context_lens)):
-        _need(t, torch.int32, name)
+        _need(t, torch.int32, name, dev)
     batch = seq_slot.shape[0]
     if out is None:
         out = _new((batch, cache.hkv, max_ctx, HEAD_DIM), torch.float32, seq_slot.device, stream)
-    desc = _desc_for(cache, out)
+    desc = _desc_for(cache, out, dev)
     if out.numel() < batch * cache.hkv * max(max_ctx, 0) * HEAD_DIM:
         raise ValueError(f"out must hold [{batch}][{cache.hkv}][{max_ctx}][{HEAD_DIM}] values, got {tuple(out.shape)}")
-    table = _ints(block_table, "block_table", cache.max_blocks_per_seq if batch else 0)
+    table = _ints(block_table, "block_table", cache.max_blocks_per_seq if batch else 0, dev)
     if batch:
         desc = _for_slots(cache, desc, block_table)
     _run(out, stream, lib().okv_dequantize, ctypes.byref(desc), batch, seq_slot.data_ptr(), table,
-         _ints(context_lens, "context_lens", batch), max_ctx, which, basis, source, out.data_ptr())
+         _ints(context_lens, "context_lens", batch, dev), max_ctx, which, basis, source, out.data_ptr())
     return out
