@@ -631,6 +631,8 @@ static DecodeArgs make_decode_args(const okv_cache_desc* d, const void* q, int B
   // grouped layouts at G = 8, and every layout at G = 16: two or four CTAs per
   // cost range, four query heads each
   a.hsplit = a.g == 16 ? 4 : (a.ng > 1 && a.g == 8) ? 2 : 1;
+  a.new_slot = a.new_pos = a.slot_lens = nullptr;
+  a.new_tokens = 0;
   return a;
 }
 
@@ -716,7 +718,11 @@ okv_status launch_decode_step(const okv_cache_desc* d, const void* k, const void
                               const int32_t* new_pos, const int32_t* slot_lens, const void* q, int B,
                               const int32_t* seq_slot, const int32_t* block_table, const int32_t* context_lens,
                               void* out, void* ws, const DecodePlan& plan, cudaStream_t s) {
-  const DecodeArgs a = make_decode_args(d, q, B, seq_slot, block_table, context_lens, out, ws, plan);
+  DecodeArgs a = make_decode_args(d, q, B, seq_slot, block_table, context_lens, out, ws, plan);
+  a.new_slot = new_slot;
+  a.new_pos = new_pos;
+  a.slot_lens = slot_lens;
+  a.new_tokens = T;
   const AppendArgs aa = make_append_args(d, k, v, new_slot, new_pos, block_table, slot_lens, nullptr);
   const int n_tiles = (T + kAppTokens - 1) / kAppTokens;
   const long long ctas = (long long)n_tiles * d->num_kv_heads * 2 + (long long)B * a.hq;

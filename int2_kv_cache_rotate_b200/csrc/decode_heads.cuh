@@ -102,6 +102,11 @@ struct DecodeArgs {
   int bits;  // bits per code: 2 or 4
   int out_bf16;
   int hsplit;  // split-K CTAs per cost range: each serves G / hsplit query heads of every KV head
+  // the tokens that the launch before this one appends (a fused step; else none)
+  const int32_t* new_slot;
+  const int32_t* new_pos;
+  const int32_t* slot_lens;
+  int new_tokens;
 };
 
 // split-K CTA count actually used: with fewer cost units than CTAs only the
@@ -404,6 +409,14 @@ __global__ void __launch_bounds__(kHW * 32, (G <= 4) ? 2 : 1) decode_heads_kerne
   // the entry holding this CTA's first cost position.
   __shared__ int part_tot[kHW], part_first[2];
   int total;
+  // a thread's token of a fused step (looked at below; loaded here and between
+  // the partition's steps, so that the loads add no latency)
+  static_assert(kFusedAppendMaxTokens <= kHW * 32, "a thread per token of the step");
+  int new_slot = -1, new_pos = 0, new_len = 0;
+  if ((int)threadIdx.x < a.new_tokens) {
+    new_slot = __ldcg(a.new_slot + threadIdx.x);
+    new_pos = __ldcg(a.new_pos + threadIdx.x);
+  }
   {
     const int per = (a.batch + blockDim.x - 1) / blockDim.x;
     const int i0 = threadIdx.x * per, i1 = min(a.batch, i0 + per);
@@ -417,6 +430,7 @@ __global__ void __launch_bounds__(kHW * 32, (G <= 4) ? 2 : 1) decode_heads_kerne
     }
     if (lane == 31) part_tot[warp] = inc;
     __syncthreads();
+    if (new_slot >= 0 && new_slot < a.num_slots) new_len = __ldcg(a.slot_lens + new_slot);
     int before = 0;
     total = 0;
 #pragma unroll
@@ -469,7 +483,10 @@ __global__ void __launch_bounds__(kHW * 32, (G <= 4) ? 2 : 1) decode_heads_kerne
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::: "memory");
   }
   asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory");
-  __syncthreads();
+  // The first copies go out while a fused step's append still runs.  Its tokens
+  // are their sequences' last ones, whose fp16 rows are read behind the wait
+  // further down; where one is written further back, among the blocks, all wait here.
+  if (__syncthreads_or(new_pos < new_len - kWin)) grid_dep_wait();
   asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory");
   constexpr int kPStride = Cfg::PS;
   uint16_t* myp = pst + warp * NGQ * HP * kPStride;  // P' tile of group k at myp + k HP kPStride
