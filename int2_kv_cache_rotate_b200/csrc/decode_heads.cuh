@@ -504,7 +504,10 @@ __global__ void __launch_bounds__(kHW * 32, (G <= 4) ? 2 : 1) decode_heads_kerne
     const bool slot_ok = slot >= 0 && slot < a.num_slots;
     const int l0 = (int)(max(start, pu) - pu), l1 = (int)(min(end, pu + us.cost) - pu);
     const size_t bh0 = (size_t)b * a.hq + (size_t)qhead0(head);  // first query head served
-    __syncthreads();  // the previous entry's window scratch / merge buffers (on the ring) are free again
+    // The previous entry's window scratch and merge buffers lie on the ring: ordinary
+    // stores and loads, which the bulk copies below (async proxy) must follow.
+    if (b != part_first[0]) fence_proxy_async();
+    __syncthreads();
     if (!slot_ok && threadIdx.x == 0) raise_flag(a.status, OKV_DEV_BAD_SLOT);
 
     // ---------------- INT2 blocks through the ring ----------------

@@ -271,6 +271,9 @@ __device__ __forceinline__ void bulk_g2s(void* dst, const void* src, uint32_t by
 __device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
 __device__ __forceinline__ void grid_dep_launch() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
 
+// orders this thread's ordinary shared-memory accesses before bulk copies issued behind a barrier
+__device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory"); }
+
 // 4-byte asynchronous global -> shared copy (no register round trip), grouped
 // per thread; cp_async_wait_all waits for this thread's groups.
 __device__ __forceinline__ void cp_async4(void* smem_dst, const void* gsrc) {
