@@ -51,3 +51,14 @@ def test_a_prepared_step_runs_on_its_tensors_device(two_devices, device, stream,
     step._fn = lambda *a: seen.append((_Device.current, a)) or okv.OK
     assert step() is step.out and _Device.current == 0
     assert seen == [(device, (1, 2, handle or 100 + device))]
+
+
+@pytest.mark.parametrize("device", [0, 1])
+@pytest.mark.parametrize("stream,handle", [(None, None), (_Stream(7), 7)])
+def test_without_torchs_private_short_cuts(two_devices, monkeypatch, device, stream, handle):
+    monkeypatch.delattr(torch._C, "_cuda_getDevice", raising=False)
+    monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream", raising=False)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: _Device.current)
+    seen = []
+    okv._run(_Tensor(device), stream, lambda *a: seen.append((_Device.current, a)) or okv.OK, 5)
+    assert seen == [(device, (5, handle or 100 + device))] and _Device.current == 0
