@@ -217,7 +217,7 @@ __device__ __forceinline__ void simt_chunk(const DecodeArgs& a, const float* qs 
       for (int wi = 0; wi < 4; ++wi) {
         // channels 64 half + 16 wi .. + 15: group (4 half + wi) ng / 8
         const uint32_t smk =
-            *reinterpret_cast<const uint32_t*>(blockp + sm_offset(a.ng, 0, tt, (4 * half + wi) * a.ng / 8));
+            *reinterpret_cast<const uint32_t*>(blockp + sm_offset(a.ng, 0, tt, (4 * half + wi) * a.ng / 8, BITS));
         const float s = __half2float(__ushort_as_half((unsigned short)(smk & 0xffff)));
         const float m = __half2float(__ushort_as_half((unsigned short)(smk >> 16)));
 #pragma unroll
@@ -578,7 +578,7 @@ static okv_status launch_decode_simt(const DecodeArgs& a, cudaStream_t s) {
 }
 
 
-bool decode_uses_tensor_cores(int g, int hkv, int ng, int bits) {
+bool decode_uses_tensor_cores(int g, int hkv, int ng) {
   const bool hkv_ok = hkv == 1 || hkv == 2 || hkv == 4 || hkv == 8;
   return hkv_ok && (ng == 1 || ng == 2 || ng == 4) && (g == 1 || g == 2 || g == 4 || g == 8 || g == 16);
 }
@@ -587,8 +587,8 @@ bool decode_uses_tensor_cores(int g, int hkv, int ng, int bits) {
 // tensor-core kernel (one at G = 8 with one group per vector, whose CTA holds
 // both n-tiles), with a range split over two (G = 8 grouped) or four (G = 16)
 // CTAs of four query heads; four CTAs per SM for the CUDA-core kernel
-int decode_ranges(int sms, int g, int hkv, int ng, int bits) {
-  if (!decode_uses_tensor_cores(g, hkv, ng, bits)) return 4 * sms;
+int decode_ranges(int sms, int g, int hkv, int ng) {
+  if (!decode_uses_tensor_cores(g, hkv, ng)) return 4 * sms;
   if (g <= 4) return 2 * sms;
   if (g == 8) return sms;
   return sms / 2;  // g = 16
@@ -656,7 +656,7 @@ static okv_status launch_decode_tail(const DecodeArgs& a, int B, cudaStream_t s)
   // predecessor; they are left out when the split-K kernel is being timed, so
   // that the events bracket it alone.
   const bool early = ev0 == nullptr;
-  const bool tc = decode_uses_tensor_cores(a.g, a.hkv, a.ng, a.bits);
+  const bool tc = decode_uses_tensor_cores(a.g, a.hkv, a.ng);
   if (tc && a.bits == 4) {
     st = launch_decode_heads_int4(a, s, early);
   } else if (tc && a.ng == 2) {

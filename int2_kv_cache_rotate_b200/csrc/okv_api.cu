@@ -94,14 +94,14 @@ okv_status validate_desc(const okv_cache_desc* d) {
 
 static size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
-DecodePlan make_decode_plan(int batch, int hq, int hkv, int ng, int bits) {
+DecodePlan make_decode_plan(int batch, int hq, int hkv, int ng) {
   DecodePlan p;
   p.batch = batch;
   p.hq = hq;
   p.hkv = hkv;
   p.g = hq / hkv;
   const int sms = device_sm_count();
-  p.num_ctas = decode_ranges(sms > 0 ? sms : 148, p.g, hkv, ng, bits);
+  p.num_ctas = decode_ranges(sms > 0 ? sms : 148, p.g, hkv, ng);
   if (p.num_ctas > 1024) p.num_ctas = 1024;  // the combine caches one weight per split
   p.num_units = batch * hkv;
   size_t off = 0;
@@ -235,7 +235,7 @@ okv_status okv_prefill_attention(const okv_cache_desc* desc, const void* q, int3
 
 size_t okv_decode_workspace_bytes(const okv_cache_desc* desc, int32_t B) {
   if (validate_desc(desc) != OKV_OK || B < 0) return 0;
-  return make_decode_plan(B, desc->num_q_heads, desc->num_kv_heads, kD / group_channels(desc), code_bits(desc)).total;
+  return make_decode_plan(B, desc->num_q_heads, desc->num_kv_heads, kD / group_channels(desc)).total;
 }
 
 okv_status okv_decode_attention(const okv_cache_desc* desc, const void* q, int32_t B,
@@ -255,7 +255,7 @@ okv_status okv_decode_attention(const okv_cache_desc* desc, const void* q, int32
     return fail(OKV_ERR_INVALID_ARG, "B * Hkv * max_blocks_per_seq too large");
   if ((uintptr_t)workspace % 256 || (uintptr_t)out % (out_bf16(desc) ? 2 : 4))
     return fail(OKV_ERR_INVALID_ARG, "workspace must be 256-byte and out element aligned");
-  const DecodePlan plan = make_decode_plan(B, desc->num_q_heads, desc->num_kv_heads, kD / group_channels(desc), code_bits(desc));
+  const DecodePlan plan = make_decode_plan(B, desc->num_q_heads, desc->num_kv_heads, kD / group_channels(desc));
   if (workspace_bytes < plan.total)
     return fail(OKV_ERR_INVALID_ARG, "workspace too small: %zu < %zu bytes", workspace_bytes, plan.total);
   return launch_decode(desc, q, B, seq_slot, block_table, context_lens, out, workspace, plan,
@@ -287,7 +287,7 @@ okv_status okv_decode_step(const okv_cache_desc* desc, const void* k, const void
     return fail(OKV_ERR_INVALID_ARG, "B * Hkv * max_blocks_per_seq too large");
   if ((uintptr_t)workspace % 256 || (uintptr_t)out % (out_bf16(desc) ? 2 : 4))
     return fail(OKV_ERR_INVALID_ARG, "workspace must be 256-byte and out element aligned");
-  const DecodePlan plan = make_decode_plan(B, desc->num_q_heads, desc->num_kv_heads, kD / group_channels(desc), code_bits(desc));
+  const DecodePlan plan = make_decode_plan(B, desc->num_q_heads, desc->num_kv_heads, kD / group_channels(desc));
   if (workspace_bytes < plan.total)
     return fail(OKV_ERR_INVALID_ARG, "workspace too small: %zu < %zu bytes", workspace_bytes, plan.total);
   const cudaStream_t s = (cudaStream_t)stream;

@@ -13,22 +13,16 @@ namespace okv {
 constexpr int kD = 128;           // head dimension
 constexpr int kBlock = 16;        // tokens per block
 constexpr int kWin = 128;         // fp16 window length
-constexpr int kBlockHeadBytes = 1152;  // one block-head with 128-channel groups
 constexpr int kKcOff = 0;         // K codes, token-major 16 x 32 B
 constexpr int kVcOff = 512;       // V codes, 4-token-interleaved chunks
 constexpr int kKsmOff = 1024;     // K (fp16 scale, fp16 min) per token (128-channel groups)
 constexpr int kVsmOff = 1088;     // V (fp16 scale, fp16 min) per token (128-channel groups)
 
-// Layout with ng = 128 / group quantisation groups per token-head (1, 2 or
-// 4): the codes as above, then K (scale, min) pairs at 1024 + 4 (t ng + k)
-// for token t, group k (channels k group .. (k + 1) group - 1), then V pairs
-// at 1024 + 64 ng + 4 (t ng + k).  ng = 1 is the layout above.
-__host__ __device__ __forceinline__ int block_head_bytes(int ng) { return 1024 + 128 * ng; }
-__host__ __device__ __forceinline__ int sm_offset(int ng, int kind, int t, int k) {
-  return 1024 + 64 * ng * kind + 4 * (t * ng + k);
-}
-// The same for codes of `bits` = 2 or 4 bits: K codes from 0, V codes from
-// 256 bits, then the pairs from 512 bits.
+// Layout with ng = 128 / group quantisation groups per token-head (1, 2 or 4)
+// and codes of `bits` = 2 or 4 bits: K codes from 0, V codes from 256 bits, then
+// from 512 bits the K (scale, min) pairs, 4 (t ng + k) bytes on for token t,
+// group k (channels k group .. (k + 1) group - 1), and 64 ng bytes further the
+// V pairs.  ng = 1 with 2 bits is the layout above.
 __host__ __device__ __forceinline__ int block_head_bytes(int ng, int bits) { return 512 * bits + 128 * ng; }
 __host__ __device__ __forceinline__ int sm_offset(int ng, int kind, int t, int k, int bits) {
   return 512 * bits + 64 * ng * kind + 4 * (t * ng + k);

@@ -67,10 +67,10 @@ constexpr int kQsStride = 8;      // floats per query head in the query-scale wo
 constexpr int kWinCost = 4;       // cost of one 16-row fp16 chunk in block units (all heads)
 constexpr int kFusedAppendMaxTokens = 127;  // okv_decode_step fuses appends this short with the query rotation
 // split-K kernel choice and residency (decode.cu)
-bool decode_uses_tensor_cores(int g, int hkv, int ng, int bits);
-int decode_ranges(int sms, int g, int hkv, int ng, int bits);
+bool decode_uses_tensor_cores(int g, int hkv, int ng);
+int decode_ranges(int sms, int g, int hkv, int ng);
 
-DecodePlan make_decode_plan(int batch, int hq, int hkv, int ng, int bits);
+DecodePlan make_decode_plan(int batch, int hq, int hkv, int ng);
 
 // bytes of one (KV head, K|V) staged R in the cache's image buffer: three bf16
 // parts x 128 x 128
