@@ -158,9 +158,13 @@ def measured_peak_bf16():
         return 1590.0, "fallback"
 
 
+# the split-K kernel, its launch and the helpers it is made of
+KERNEL_SOURCES = ("decode.cu", "decode_heads.cuh", "okv_common.cuh")
+
+
 def kernel_source_hash():
     h = hashlib.sha256()
-    for name in ("decode.cu", "okv_common.cuh"):
+    for name in KERNEL_SOURCES:
         with open(os.path.join(ROOT, "int2_kv_cache_rotate_b200", "csrc", name), "rb") as f:
             h.update(f.read())
     return h.hexdigest()[:16]
