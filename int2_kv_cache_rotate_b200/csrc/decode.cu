@@ -372,7 +372,7 @@ __global__ void __launch_bounds__(kDecWarps * 32) decode_simt_kernel(DecodeArgs 
 #pragma unroll
         for (int j = 0; j < 4; ++j) mo[(warp * G + gg) * kD + 4 * lane + j] = st.o[gg][j];
         if (lane == 0) {
-          ml[(warp * G + gg) * 2 + 0] = st.m[gg];
+          ml[(warp * G + gg) * 2 + 0] = merge_max(st.m[gg], st.l[gg]);
           ml[(warp * G + gg) * 2 + 1] = st.l[gg];
         }
       }
@@ -383,11 +383,13 @@ __global__ void __launch_bounds__(kDecWarps * 32) decode_simt_kernel(DecodeArgs 
         float mx = -INFINITY;
         for (int w = 0; w < kDecWarps; ++w) mx = fmaxf(mx, ml[(w * G + gg) * 2]);
         float o = 0.f, l = 0.f;
-        for (int w = 0; w < kDecWarps; ++w) {
-          const float mw = ml[(w * G + gg) * 2], lw = ml[(w * G + gg) * 2 + 1];
-          const float sc = lw == 0.f ? 0.f : exp2f(mw - mx);  // (a sum that is NaN goes on to the output)
-          o = fmaf(mo[(w * G + gg) * kD + ch], sc, o);
-          l = fmaf(lw, sc, l);
+        if (mx != -INFINITY) {
+          for (int w = 0; w < kDecWarps; ++w) {
+            const float mw = ml[(w * G + gg) * 2];
+            const float sc = (mw == -INFINITY) ? 0.f : exp2f(mw - mx);
+            o = fmaf(mo[(w * G + gg) * kD + ch], sc, o);
+            l = fmaf(ml[(w * G + gg) * 2 + 1], sc, l);
+          }
         }
         dst[gg * kPartStride + ch] = o;
         if (ch == 0) {
@@ -480,11 +482,10 @@ __global__ void __launch_bounds__(kCombThreads) combine_kernel(DecodeArgs a) {
   for (int w = 1; w < kCombWarps; ++w) mx = fmaxf(mx, redm[w]);
   float l = 0.f;
   for (int c = tid; c < ns; c += kCombThreads) {
-    // a split without a key has sum 0 and maximum -inf; a sum that is NaN (a
-    // query or a token that is not finite) goes on to the output
-    const float lc = wsum[c], w = lc == 0.f ? 0.f : exp2f(ml[c] - mx);
+    const float m = ml[c];
+    const float w = (mx == -INFINITY || m == -INFINITY) ? 0.f : exp2f(m - mx);
     ml[c] = w;
-    l = fmaf(lc, w, l);
+    l = fmaf(wsum[c], w, l);
   }
   l = warp_sum(l);
   if (lane == 0) redl[warp] = l;

@@ -78,6 +78,12 @@ __device__ __forceinline__ int clamp_len_cg(const int32_t* context_lens, int b, 
   return len;
 }
 
+// The maximum that goes with a piece's sum of weights into a merge.  A query or
+// token that is not finite makes the sum NaN and leaves the maximum anywhere; with
+// +inf in its place the piece's weight is exp2(inf - inf), so that NaN reaches the
+// output instead of a piece that looks empty (maximum -inf).
+__device__ __forceinline__ float merge_max(float m, float l) { return l != l ? INFINITY : m; }
+
 struct DecodeArgs {
   const __nv_bfloat16* q;
   const int32_t* seq_slot;
@@ -1635,7 +1641,7 @@ __global__ void __launch_bounds__(kHW * 32, (G <= 4) ? 2 : 1) decode_heads_kerne
             }
           }
           if (g == 0) {
-            part_b[(size_t)hs * kPartStride + 128] = st.m[nt];
+            part_b[(size_t)hs * kPartStride + 128] = merge_max(st.m[nt], l);
             part_b[(size_t)hs * kPartStride + 129] = l;
           }
         }
@@ -1661,7 +1667,7 @@ __global__ void __launch_bounds__(kHW * 32, (G <= 4) ? 2 : 1) decode_heads_kerne
 #pragma unroll
           for (int i = 0; i < 16; ++i) dst[col_chan<NGQ, BITS>(g, i)] = v[i] + ms[col_group<NGQ, BITS>(i)];
           if (g == 0) {
-            ml[(warp * G + hs) * 2 + 0] = st.m[nt];
+            ml[(warp * G + hs) * 2 + 0] = merge_max(st.m[nt], l);
             ml[(warp * G + hs) * 2 + 1] = l;
           }
         }
@@ -1673,13 +1679,15 @@ __global__ void __launch_bounds__(kHW * 32, (G <= 4) ? 2 : 1) decode_heads_kerne
         float mx = -INFINITY;
         for (int k = 0; k < wph; ++k) mx = fmaxf(mx, ml[((hh + k * hkv) * G + gg) * 2]);
         float o = 0.f, l = 0.f;
-        for (int k = 0; k < wph; ++k) {
-          const int w = hh + k * hkv;
-          const float mw = ml[(w * G + gg) * 2], lw = ml[(w * G + gg) * 2 + 1];
-          if (lw == 0.f) continue;  // a warp that saw no key (a sum that is NaN goes on to the output)
-          const float sc = exp2f(mw - mx);
-          o = fmaf(mo[((size_t)w * G + gg) * kD + ch], sc, o);
-          l = fmaf(lw, sc, l);
+        if (mx != -INFINITY) {
+          for (int k = 0; k < wph; ++k) {
+            const int w = hh + k * hkv;
+            const float mw = ml[(w * G + gg) * 2];
+            if (mw == -INFINITY) continue;
+            const float sc = exp2f(mw - mx);
+            o = fmaf(mo[((size_t)w * G + gg) * kD + ch], sc, o);
+            l = fmaf(ml[(w * G + gg) * 2 + 1], sc, l);
+          }
         }
         float* dst = a.part + ((size_t)(crange() + b) * a.hq + (size_t)qhead0(hh) + gg) * kPartStride;
         dst[ch] = o;
