@@ -1149,8 +1149,12 @@ __global__ void __launch_bounds__(kHW * 32, (G <= 4) ? 2 : 1) decode_heads_kerne
       // Bound by bytes with one group and G = 4 (4 sequences of 100K: 435 MB in 81
       // us, 5.4 TB/s, 82 % of a plain copy; a first form on the CUDA cores 608 a
       // step), by the latency of a step's chain with G = 8 (1 of 131K, eight warps
-      // an SM: 142 MB in 50 us) and by the groups' arithmetic with more (16 of 1K to
-      // 32K, two groups: 188 MB in 49 us).
+      // an SM at 254 registers: 142 MB in 50 us).  With more groups it is bound by
+      // their arithmetic and by registers: 4 of 100K take 92 us a step with two
+      // groups and 108 with four where one takes 84, for 6 and 18 % more bytes, and
+      // at 128 registers a thread the grouped forms spill 24 to 60 bytes (one group
+      // none).  The ragged batch of 16 shows its partition apart from that: 52 us
+      // with one group for 178 MB, 57 with two for 188.
       auto step4 = [&](auto full_tag) {
         constexpr bool fullstep = decltype(full_tag)::value;
         const unsigned char* s0 = ring + s * kStageBytes + q0 * copy_bytes + head * BHB;

@@ -571,7 +571,10 @@ class AppendPlan:
       free_count         int32 [1]: blocks left in the pool
 
     The buffers stay the same from call to call, so a step can be captured in a
-    CUDA graph.  Two plans (or a plan built on two streams) share nothing."""
+    CUDA graph.  They are one set per plan, workspace included: builds of one
+    plan, captured ones among them, have to follow one another.  Steps that are
+    built at the same time, on two streams, take a plan each (two plans share
+    nothing)."""
 
     def __init__(self, batch: int, max_tokens: int, device="cuda"):
         import torch
