@@ -119,8 +119,13 @@ typedef enum {
  * bf16 instead of fp32, 2-byte aligned (16 for okv_dequantize).  A decode or
  * gather rounds the same fp32 result once.  A prefill over 4-bit codes then
  * also reads q~, the dequantised keys and values (saturating at +-65504, like
- * the cache's fp16 rows) and the softmax weights as fp16, each rounded once:
- * one matrix product where fp32 output takes two.  It is a property of the
+ * the cache's fp16 rows) and the softmax weights as fp16, each rounded once
+ * (2^-11 of it; a weight again each time that its row's running maximum moves
+ * in the same 128 keys): one matrix product where fp32 output takes two.  With
+ * the cache's staged image, q~ comes from R_K as two bf16 parts (2^-16 of it),
+ * and with 64 rows (T Hq) per SM or more and a 16-byte aligned output the
+ * normalised rows are rounded to fp16 under a scale of their own (2^-11 of a
+ * value) before the product with U_V as two fp16 parts.  It is a property of the
  * call, not of the cache: the same buffers serve both.
  * OKV_PAD_ROWS: appended rows (and gathered sequences) whose sequence slot is
  * exactly -1 are skipped without OKV_DEV_BAD_SLOT, as okv_plan_append leaves

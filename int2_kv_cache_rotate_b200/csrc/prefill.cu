@@ -1325,8 +1325,9 @@ okv_status launch_prefill(const okv_cache_desc* d, const void* q, int T, int slo
     st = check_launch("prefill attention");
   }
   if (st != OKV_OK) return st;
-  // (fewer rows than 64 per SM leave too few CTAs of 128: 16 tokens over 8K keys 96 us there against 50; 296 tokens,
-  // just above, 110 against 125)
+  // Fewer rows than 64 per SM leave too few CTAs of 128.  Both ways over 8K keys, tensor cores and CUDA cores, us a
+  // prefill: 32/8 heads 16 tokens 96 and 50, 148 102 and 84, 222 111 and 102, 295 (the last below) 123 and 122, 296
+  // 123 and 122, 370 131 and 138, 592 175 and 198; 64/8, 40/5 and 8/2 heads meet within 1 % at the switch as well.
   if (int4_bf16 && !small && (uintptr_t)out % 16 == 0) return launch_prefill_unrotate_int4(a, sp, s);
   // The un-rotation may start (programmatic launch) while the attention's last
   // CTAs run: it stages U_V, then waits for the attention's outputs.  Starting

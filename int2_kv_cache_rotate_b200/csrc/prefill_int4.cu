@@ -1,10 +1,10 @@
 // Chunked-prefill attention over the 4-bit cache with bf16 output, on the
 // tcgen05 tensor cores.
 //
-// bf16 output leaves 2^-9 of a value, so one fp16 operand per factor is
+// bf16 output leaves 2^-8 of a value, so one fp16 operand per factor is
 // enough: q~ 2^-e is rounded to fp16 once, keys and values are dequantised
 // once, s c + m rounded to fp16 by one half-precision FMA, and the softmax
-// weight p 2^11 is rounded to fp16.  Each rounding is 2^-12 of its operand at
+// weight p 2^11 is rounded to fp16.  Each rounding is 2^-11 of its operand at
 // most and independent from key to key.  (fp32 output takes the kernel of
 // prefill.cu: two fp16 halves of q~ and of p s against exact codes.)  The
 // group's scale and minimum are gone after staging, so the softmax has no
@@ -36,9 +36,12 @@
 // columns and in the value tile alike.
 // Bound: 128 keys x 256 rows cost 32 MMAs of 64 cycles and 32768 exponentials
 // at 16 a cycle, 2048 cycles each; a chunk takes 5250 (1024 tokens over 32K keys,
-// 32/8 heads: 640 us, 845 TFLOP/s), the exponential unit and the tensor pipe
-// 39 % busy, issue slots 45 %: what is left is the latency of each tile's chain
-// of scores, softmax and value MMA.  One range of work per SM against one tile
+// 32/8 heads: 640 us, 845 TFLOP/s), so that either unit is 39 % busy, which is
+// also what the counters say, and issue slots 45 %: what is left is the latency
+// of each tile's chain of scores, softmax and value MMA.  64-channel groups take
+// the same time (694 us a call against 688); with 32 channels the staging's
+// pairs push the kernel past 128 registers (112 bytes of spills) and a call
+// takes 846.  One range of work per SM against one tile
 // per CTA (128 of them): 762 against 873 us a call.  Not taken (same call, 762):
 // the value MMA of the first 64 keys started while the softmax does the others
 // 847 (the issuing warp then waits where the other tile could go on), a warp of

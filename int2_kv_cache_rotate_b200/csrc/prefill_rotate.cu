@@ -6,14 +6,14 @@
 // 16-bit parts (32 MMAs of K 16 per 256 rows), and both round their result's
 // or their input's rows once:
 //   query  A = q (bf16, exact), B = R_K as the first two bf16 parts of the
-//          cache's staged image (2^-17 of it); the row is scaled by 2^-e and
+//          cache's staged image (2^-16 of it); the row is scaled by 2^-e and
 //          rounded to fp16, which is what the attention takes;
 //   output the merged row is normalised, goes through the butterfly in
-//          registers in fp32 and, scaled by 2^-e, to fp16 (2^-12 of a value,
+//          registers in fp32 and, scaled by 2^-e, to fp16 (2^-11 of a value,
 //          an eighth of a bf16 output's rounding), B = U_V as two fp16 parts.
 // Bound: the latency of load, product and store one after the other, and behind
 // the attention the bytes (32768 rows: 17 MB, and up to three pieces of each).
-// 32768 rows take 10 us before the attention (39 on the CUDA cores) and 35
+// 32768 rows take 10 us before the attention (39 on the CUDA cores) and 36
 // behind it (45 and more); fp32 output and the 2-bit cache keep the CUDA cores,
 // whose fp32 products their smaller tolerances count on.
 #include "okv_common.cuh"
