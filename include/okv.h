@@ -462,7 +462,9 @@ okv_status okv_plan_append(const okv_plan* plan, void* workspace, size_t workspa
  *   position is padding, its outputs stay as they are; inv_freq: device fp32
  *   [rot_dim/2]; q_weight, k_weight: device fp32 [128], NULL = 1.
  * Angles are formed and reduced in fp64, sums and products are fp32, outputs
- * are rounded once.  One launch.  Errors: INVALID_ARG (NULL, sizes, alignment,
+ * are rounded once.  A norm takes rows whose squares fp32 holds: values up to
+ * 10^18, and with eps = 0 not all below 10^-18 (fp16 rows always do).  One
+ * launch.  Errors: INVALID_ARG (NULL, sizes, alignment,
  * eps outside [0, 1], rope_scale not positive), UNSUPPORTED (head_dim != 128,
  * rot_dim not a multiple of 16 up to 128, unknown in_type).
  * Pages: gen-hub.ru "Что придумали в Together AI" (the rotations apply to the
